@@ -10,3 +10,6 @@ from .abi import (  # noqa: F401
     DlrmError, DlrmModel, DlrmPlan, dlrm_emb_interact, dlrm_emb_interact_dots, dlrm_emb_interact_pool, dlrm_forward,
     dlrm_forward_workspace_bytes, dlrm_interact_lower_tri, emb_bag_pool, emb_bag_sum_multi,
     linear_bias_act, linear_bias_act_split, load, mlp_forward)
+from .token_ops import (  # noqa: F401
+    emb_lookup_grad, emb_lookup_grad_workspace_bytes, emb_lookup_scaled, linear_i8_bias_act,
+    rms_norm_residual_i8)

@@ -34,7 +34,9 @@ EXPORTS = ("dlrm_status_string", "dlrm_abi_version", "dlrm_set_kernel_timing_eve
            "linear_bias_act_split", "linear_bias_act_head", "mlp_forward",
            "dlrm_forward_workspace_bytes", "dlrm_forward", "dlrm_forward_noalloc",
            "dlrm_plan_create",
-           "dlrm_plan_update", "dlrm_plan_run", "dlrm_plan_destroy")
+           "dlrm_plan_update", "dlrm_plan_run", "dlrm_plan_destroy",
+           "emb_lookup_scaled", "emb_lookup_grad_workspace_bytes", "emb_lookup_grad",
+           "rms_norm_residual_i8", "linear_i8_bias_act")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -134,6 +136,21 @@ def load(path: str = LIB_PATH):
     lib.dlrm_plan_run.argtypes = [_vp, _vp]
     lib.dlrm_plan_destroy.restype = ctypes.c_int
     lib.dlrm_plan_destroy.argtypes = [_vp]
+    f32, f64, size = ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+    lib.emb_lookup_scaled.restype = ctypes.c_int
+    lib.emb_lookup_scaled.argtypes = [_i64, _i64, _i32, _vp, _i64, _i32, _vp, f32, _vp, _i64,
+                                      _i32, _vp]
+    lib.emb_lookup_grad_workspace_bytes.restype = size
+    lib.emb_lookup_grad_workspace_bytes.argtypes = [_i64, _i64, _i32]
+    lib.emb_lookup_grad.restype = ctypes.c_int
+    lib.emb_lookup_grad.argtypes = [_i64, _i64, _i32, _vp, _i64, _i32, _vp, f32, _i32, _vp,
+                                    _i64, _i32, _vp, size, _vp]
+    lib.rms_norm_residual_i8.restype = ctypes.c_int
+    lib.rms_norm_residual_i8.argtypes = [_i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp, f64, _vp,
+                                         _i64, _vp, _i64, _vp, _vp]
+    lib.linear_i8_bias_act.restype = ctypes.c_int
+    lib.linear_i8_bias_act.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                                       _i32, _vp, _i64, _i32, _vp]
     if path == LIB_PATH:
         _LIB = lib
     return lib

@@ -211,4 +211,68 @@ hipError_t launch_linear_head(int M, int N, int K, const float *A, int64_t lda, 
                               const float *head_bias, int head_act, float *out, int64_t ldo,
                               hipStream_t stream);
 
+// ------------------------------------------------------ token operators --
+
+// Scaled lookup of single tokens (token_lookup.hip).
+struct LookupParams {
+  int64_t tokens, rows;
+  int dim;
+  const void *table;  // rows of dim elements, ld_table apart
+  int64_t ld_table;
+  const int32_t *token;
+  float scale;
+  void *out;
+  int64_t ld_out;
+};
+hipError_t launch_lookup(const LookupParams &p, int table_dtype, int out_dtype,
+                         hipStream_t stream);
+
+// Its gradient (token_grad.hip).
+struct GradParams {
+  int64_t n, rows;  // tokens, table rows
+  int dim;
+  const void *grad;  // (n, dim), rows ld_grad apart
+  int64_t ld_grad;
+  const int32_t *token;
+  float scale;
+  void *out;  // (rows, dim), rows ld_out apart
+  int64_t ld_out;
+  int accumulate;
+};
+size_t lookup_grad_workspace(int64_t n, int64_t rows, int dim);
+hipError_t launch_lookup_grad(const GradParams &p, int grad_dtype, int out_dtype, void *ws,
+                              hipStream_t stream);
+
+// Residual addition, RMS norm and int8 codes (rms_norm_i8.hip).
+struct NormParams {
+  int64_t m;
+  int dim;
+  const void *x, *residual;  // residual may be null
+  int64_t ldx, ldr;
+  const float *weight;       // (dim,) or null
+  double eps;
+  void *h;                   // written when there is a residual
+  int64_t ldh;
+  int8_t *codes;
+  int64_t ldq;
+  float *scale;              // (m,)
+};
+hipError_t launch_rms_norm_i8(const NormParams &p, int dtype, hipStream_t stream);
+
+// int8 product with a scale for each row of A and of W (linear_i8.hip).
+struct LinearI8Params {
+  int M, N, K;
+  const int8_t *A;
+  int64_t lda;
+  const float *a_scale;  // (M,)
+  const int8_t *W;       // (N, K), rows ldw apart
+  int64_t ldw;
+  const float *w_scale;  // (N,)
+  const float *bias;     // (N,) or null
+  int act;
+  void *C;
+  int64_t ldc;
+};
+hipError_t launch_linear_i8(const LinearI8Params &p, int out_dtype, hipStream_t stream);
+
 }  // namespace dlrm

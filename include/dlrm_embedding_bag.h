@@ -555,6 +555,114 @@ DLRM_API int dlrm_plan_update(dlrm_plan *plan, const float *dense_in,
 DLRM_API int dlrm_plan_run(dlrm_plan *plan, void *stream);
 DLRM_API int dlrm_plan_destroy(dlrm_plan *plan);
 
+/* ------------------------------------------------------------------------
+ * Token operators: embedding lookup of single tokens with a scale and its
+ * gradient, RMS norm of rows with int8 codes, and the int8 product that
+ * reads them.  They follow the conventions at the top of this header, and
+ *  - rows may be strided and may start at any element: alignment and odd
+ *    lengths take the same code;
+ *  - the row stride of an input may be 0 (one row, repeated); an output's is
+ *    at least its row length;
+ *  - token values are checked on the device: one outside [0, rows) (padding,
+ *    usually -1) reads as a row of zeros and has no gradient.
+ */
+#define DLRM_MAX_TOKEN_DIM (1 << 20) /* row length of the lookup and the norm */
+
+/*
+ * emb_lookup_scaled -- out[t, :] = scale * table[tokens[t], :], the product in
+ * float32, rounded once to the output type; zeros for a token outside
+ * [0, rows), whatever the scale.
+ *
+ *   num_tokens  0 <= num_tokens <= INT32_MAX (0: nothing to do)
+ *   rows, dim   1 <= rows < INT32_MAX, 1 <= dim <= DLRM_MAX_TOKEN_DIM
+ *   table       (rows, dim) of table_dtype (float32, bfloat16, FP8 E4M3),
+ *               row stride ld_table
+ *   tokens      (num_tokens,) int32
+ *   out         (num_tokens, dim) of out_dtype (float32, bfloat16), row
+ *               stride ld_out
+ */
+DLRM_API int emb_lookup_scaled(int64_t num_tokens, int64_t rows, int32_t dim, const void *table,
+                               int64_t ld_table, int32_t table_dtype, const int32_t *tokens,
+                               float scale, void *out, int64_t ld_out, int32_t out_dtype,
+                               void *stream);
+
+/*
+ * emb_lookup_grad -- the gradient of emb_lookup_scaled with respect to the
+ * table:
+ *   out[r, :] = base + scale * sum over t with tokens[t] == r of grad[t, :]
+ * with base 0 (accumulate 0: every row of out is written) or out[r, :]
+ * (accumulate 1: rows that no token names are not touched).  Sums run in
+ * float32 over a row's tokens in an order that depends on the arguments'
+ * values only, so equal calls give equal bits; each element is rounded once
+ * to out_dtype.  With a negative learning rate as scale and the table as out
+ * this is a step of gradient descent in place.
+ *
+ *   grad        (num_tokens, dim) of grad_dtype (float32, bfloat16), row
+ *               stride ld_grad
+ *   tokens      (num_tokens,) int32
+ *   out         (rows, dim) of out_dtype (float32, bfloat16), row stride
+ *               ld_out; must not overlap grad
+ *   workspace   16-byte aligned, at least
+ *               emb_lookup_grad_workspace_bytes(num_tokens, rows, dim) bytes
+ *               (which returns 0 for sizes that the call refuses); its
+ *               content needs no clearing and carries nothing to the next
+ *               call
+ */
+DLRM_API size_t emb_lookup_grad_workspace_bytes(int64_t num_tokens, int64_t rows, int32_t dim);
+DLRM_API int emb_lookup_grad(int64_t num_tokens, int64_t rows, int32_t dim, const void *grad,
+                             int64_t ld_grad, int32_t grad_dtype, const int32_t *tokens,
+                             float scale, int32_t accumulate, void *out, int64_t ld_out,
+                             int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * rms_norm_residual_i8 -- for each row:
+ *   h = x + residual, rounded to dtype      (h = x without a residual)
+ *   y = h * weight / sqrt(mean(h^2) + eps)  (float64)
+ *   scale = max|y| / 127                    (rounded to float32)
+ *   codes = round(y / scale)                (ties to even, within +-127)
+ * so codes * scale stands for y.  A row of zeros has scale 0 and codes 0.  A
+ * row that holds an infinity or a NaN, or that meets a weight that does, has
+ * scale NaN and codes 0; other rows are not affected.
+ *
+ *   m >= 0 (0: nothing to do), 1 <= dim <= DLRM_MAX_TOKEN_DIM
+ *   x, residual  (m, dim) of dtype (float32, bfloat16), row strides ldx, ldr;
+ *                residual may be NULL
+ *   weight       (dim,) float32, or NULL for ones
+ *   eps          finite, >= 0
+ *   h            (m, dim) of dtype, row stride ldh: written when there is a
+ *                residual, else not used and may be NULL.  It may be x or
+ *                residual itself (same pointer and stride)
+ *   codes        (m, dim) int8, row stride ldq
+ *   scale        (m,) float32
+ */
+DLRM_API int rms_norm_residual_i8(int64_t m, int32_t dim, const void *x, int64_t ldx,
+                                  const void *residual, int64_t ldr, int32_t dtype,
+                                  const float *weight, double eps, void *h, int64_t ldh,
+                                  int8_t *codes, int64_t ldq, float *scale, void *stream);
+
+/*
+ * linear_i8_bias_act -- linear_bias_act of int8 operands with a scale for
+ * each row of a (token) and of w (channel):
+ *   c[m, n] = act(bias[n] + a_scale[m] w_scale[n] sum_k a[m, k] w[n, k])
+ * The sum over k is exact; it is rounded to float32, scaled, and the result
+ * rounded once to out_dtype.
+ *
+ *   m >= 0 (0: nothing to do), n >= 1, 1 <= k <= 131071 (beyond it the int32
+ *   sum could overflow: DLRM_ERR_UNSUPPORTED, as for m or n above 2^26)
+ *   a        (m, k) int8, row stride lda
+ *   a_scale  (m,) float32
+ *   w        (n, k) int8, row stride ldw >= k
+ *   w_scale  (n,) float32
+ *   bias     (n,) float32, or NULL for no bias
+ *   act      a dlrm_act
+ *   c        (m, n) of out_dtype (float32, bfloat16), row stride ldc
+ */
+DLRM_API int linear_i8_bias_act(int32_t m, int32_t n, int32_t k, const int8_t *a, int64_t lda,
+                                const float *a_scale, const int8_t *w, int64_t ldw,
+                                const float *w_scale, const float *bias, int32_t act, void *c,
+                                int64_t ldc, int32_t out_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,7 +24,7 @@ constexpr int kChunks = kBK / 16;
 constexpr int kXcds = 8;
 
 __device__ __forceinline__ float apply_act(float x, int act) {
-  if (act == 1) return x > 0.0f ? x : 0.0f;
+  if (act == 1) return x <= 0.0f ? 0.0f : x;  // NaN (a row without a scale) stays
   if (act == 2) return 1.0f / (1.0f + expf(-x));
   return x;
 }

@@ -58,7 +58,9 @@ struct RowScale {
   double f;
 };
 __device__ __forceinline__ RowScale row_scale(double ss, double mx, int dim, double eps) {
-  const double r = 1.0 / sqrt(ss / dim + eps);
+  // an infinite sum (an infinity in the row) leaves no value, also where every
+  // product h * weight that is compared is finite
+  const double r = ss < INFINITY ? 1.0 / sqrt(ss / dim + eps) : NAN;
   RowScale o;
   o.s = (float)(mx * r / 127.0);
   o.f = (o.s > 0.0f && o.s < INFINITY) ? r / (double)o.s : 0.0;

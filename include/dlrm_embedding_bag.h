@@ -621,9 +621,10 @@ DLRM_API int emb_lookup_grad(int64_t num_tokens, int64_t rows, int32_t dim, cons
  *   y = h * weight / sqrt(mean(h^2) + eps)  (float64)
  *   scale = max|y| / 127                    (rounded to float32)
  *   codes = round(y / scale)                (ties to even, within +-127)
- * so codes * scale stands for y.  A row of zeros has scale 0 and codes 0.  A
- * row that holds an infinity or a NaN, or that meets a weight that does, has
- * scale NaN and codes 0; other rows are not affected.
+ * so codes * scale stands for y.  A row of zeros has scale 0 and codes 0
+ * (with eps 0 it has no norm: scale NaN).  A row that holds an infinity or a
+ * NaN, or that meets a weight that does, has scale NaN and codes 0; other
+ * rows are not affected.
  *
  *   m >= 0 (0: nothing to do), 1 <= dim <= DLRM_MAX_TOKEN_DIM
  *   x, residual  (m, dim) of dtype (float32, bfloat16), row strides ldx, ldr;
@@ -646,7 +647,8 @@ DLRM_API int rms_norm_residual_i8(int64_t m, int32_t dim, const void *x, int64_t
  * each row of a (token) and of w (channel):
  *   c[m, n] = act(bias[n] + a_scale[m] w_scale[n] sum_k a[m, k] w[n, k])
  * The sum over k is exact; it is rounded to float32, scaled, and the result
- * rounded once to out_dtype.
+ * rounded once to out_dtype.  A NaN scale leaves NaN in its row or column,
+ * through every act.
  *
  *   m >= 0 (0: nothing to do), n >= 1, 1 <= k <= 131071 (beyond it the int32
  *   sum could overflow: DLRM_ERR_UNSUPPORTED, as for m or n above 2^26)

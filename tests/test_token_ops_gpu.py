@@ -348,6 +348,11 @@ def test_norm_rows_that_are_not_finite_or_zero(dim):
     w[0] = float("inf")
     _, q, s = fw.rms_norm_residual_i8(x[7:8].cuda(), w.cuda())
     assert torch.isnan(s).all() and torch.all(q == 0)
+    # an infinity that meets a weight of zero: inf * 0
+    w[0] = 0.0
+    x[1, dim // 2], x[1, 0] = 1.0, float("inf")
+    _, q, s = fw.rms_norm_residual_i8(x[1:2].cuda(), w.cuda())
+    assert torch.isnan(s).all() and torch.all(q == 0)
     # weights of zero: zero rows
     _, q, s = fw.rms_norm_residual_i8(x[7:8].cuda(), torch.zeros(dim).cuda())
     assert float(s) == 0.0 and torch.all(q == 0)
@@ -481,6 +486,22 @@ def test_product_strides(m, n, k):
     got = fw.linear_i8_bias_act(flat[1:].view(m, k), sa.cuda(), w.cuda(), sw.cuda())
     _check_product(got, a, sa, w, sw, None, "none", "f32")
     assert fw.linear_i8_bias_act(a[:0].cuda(), sa[:0].cuda(), w.cuda(), sw.cuda()).shape == (0, n)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 40, 100), (200, 130, 300)])
+def test_product_rows_without_a_scale(m, n, k):
+    """A row that the norm could not scale (NaN) stays visible after every act,
+    and its neighbours are not affected."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    a, sa, w, sw, b = _product_case(m, n, k, 11)
+    a[1], sa[1] = 0, float("nan")
+    keep = [i for i in range(m) if i != 1]
+    for act in ("none", "relu", "sigmoid"):
+        got = fw.linear_i8_bias_act(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), b.cuda(), act)
+        assert torch.isnan(got[1]).all()
+        _check_product(got[keep], a[keep], sa[keep], w, sw, b, act, "f32")
 
 
 # ------------------------------------------------------- streams and graphs --

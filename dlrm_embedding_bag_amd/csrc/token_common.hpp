@@ -150,4 +150,34 @@ __device__ __forceinline__ void store_chunk(typename T::S *row, int c, int dim,
   }
 }
 
+// Eight elements as they were read, for loads that wait in registers: half the
+// registers of float32 for bfloat16 rows.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<F32> {
+  float v[8];
+  __device__ __forceinline__ void load(const float *row, int c, int dim) {
+    load_chunk<F32>(row, c, dim, v);
+  }
+  __device__ __forceinline__ float at(int e) const { return v[e]; }
+};
+template <>
+struct Chunk<BF16> {
+  u32x4_t v;
+  __device__ __forceinline__ void load(const uint16_t *row, int c, int dim) {
+    if (c + 8 <= dim) {
+      v = (u32x4_t) * reinterpret_cast<const u32x4_u *>(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = (c + 2 * e < dim ? (uint32_t)row[c + 2 * e] : 0) |
+               (c + 2 * e + 1 < dim ? (uint32_t)row[c + 2 * e + 1] << 16 : 0);
+    }
+  }
+  __device__ __forceinline__ float at(int e) const {
+    return e & 1 ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]);
+  }
+};
+
 }  // namespace dlrm

@@ -3,25 +3,32 @@
 //   out[r, :] = (out[r, :] or 0) + scale * sum over t with token[t] == r of grad[t, :]
 //
 // Tokens outside [0, rows) add nothing.  The sum of a row runs over its
-// tokens in a fixed order, in float32, so equal inputs give equal bits; no
-// floating-point atomic is used.
+// tokens in an order that the tokens alone decide, in float32, so equal inputs
+// give equal bits; no floating-point atomic is used.
 //
-// Tokens are sorted by row with their positions (a stable radix sort, least
-// significant digit first), so the tokens of a row are neighbours.  Then the
-// sorted order is cut into chunks of equal length, whatever the rows'
-// frequencies: a lane group adds up one chunk's gradient rows and stores each
-// row that begins and ends inside it.  A row whose tokens cross a border
-// leaves partial sums (one per chunk it touches), which the last launch adds
-// in chunk order.  A token that fills a tenth of the batch is thus as well
-// spread over the chip as rare ones.
+// Tokens are sorted by row, equal ones by position, so the tokens of a row are
+// neighbours; then the sorted order is cut into equal parts, whatever the
+// rows' frequencies, so that a token that fills a tenth of the batch is as
+// well spread over the chip as rare ones.
 //
-// Digits of the sort: the key's bits are divided evenly over passes of at
-// most kMaxDigit bits.  A pass is a histogram per tile of tokens and a
-// scatter, in which every tile adds up the histogram for itself (bins x tiles
-// counts, read from L2) instead of waiting for a scan launch.
+// Up to kTile tokens, one launch does everything: each of its workgroups
+// sorts all tokens in its registers and LDS (none waits for another) and adds
+// up its share of the sorted order; others write zeros to the rows that no
+// token names.
 //
+// Beyond, four launches (five or six for millions of tokens):
+//   tile_sort   tiles of kTile tokens, each sorted by one workgroup
+//   merge       a token's place among up to kMaxFan sorted runs is its place
+//               in its own run plus, for each other run, a binary search:
+//               thousands of independent searches that stay in the caches,
+//               in one launch where a radix sort takes two for each digit
+//   reduce      workgroups add up equal parts of the sorted order; a row that
+//               crosses a border leaves partial sums
+//   fix         adds those in order
 // Without accumulate every row of out is written: the sort's launches occupy
 // few CUs, so their grids carry further workgroups that fill out with zeros.
+#include <type_traits>
+
 #include "kernels.hpp"
 #include "token_common.hpp"
 
@@ -29,77 +36,199 @@ namespace dlrm {
 
 namespace {
 
-constexpr int kMaxDigit = 10;
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kItems = 4;                       // per thread
-constexpr int kTile = kSortThreads * kItems;    // tokens sorted at once by a workgroup
-constexpr int kMaxTiles = 512;                  // sorting workgroups (of one or more kTile)
-constexpr int kFillBlocks = 512;                // zero-filling workgroups per launch
-constexpr int kUnroll = 8;                      // gradient rows in flight per lane group
-constexpr int kFixThreads = 512;
-constexpr int kShortParts = 8;                  // chunks one lane group adds up alone
+constexpr int kThreads = 512;                 // of a sorting workgroup
+constexpr int kWaves = kThreads / kWave;
+constexpr int kFew = 2;                       // tokens of a thread that sorts few,
+constexpr int kMany = 4;                      // and many
+constexpr int kTile = kMany * kThreads;       // tokens that one workgroup sorts
+constexpr int kOneMerge = 32;                 // runs merged at once where that ends it,
+constexpr int kMaxFan = 16;                   // and else
+constexpr int kMergeWaves = 8;
+constexpr int kMergeThreads = kMergeWaves * kWave;
+constexpr int kSearches = 4;                  // binary searches of a thread in flight
+constexpr int kFillBlocks = 2048;             // zero-filling workgroups per launch
+constexpr int kReduceThreads = 256;
+constexpr int kMaxPer = 8;                    // tokens that a lane group adds up alone
+constexpr int kFixThreads = 256;
+constexpr int kUnroll = 8;                    // partial sums of a lane group in flight
+constexpr int64_t kMaxBlocks = 1 << 22;       // a launch holds fewer than 2^32 threads
 
-struct SortPlan {
-  int passes, digit;
-  int tiles, rounds;  // sorting workgroups, and the kTile tokens each takes in turn
-};
+// ------------------------------------------------------------------ sort --
 
-SortPlan plan_sort(int64_t n, int64_t rows) {
-  int bits = 1;
-  while ((rows >> bits) != 0) ++bits;  // keys are 0 .. rows (rows: not there)
-  SortPlan s;
-  s.passes = (bits + kMaxDigit - 1) / kMaxDigit;
-  s.digit = (bits + s.passes - 1) / s.passes;
-  const int64_t all = (n + kTile - 1) / kTile;
-  s.rounds = (int)((all + kMaxTiles - 1) / kMaxTiles);
-  s.tiles = s.rounds ? (int)((all + s.rounds - 1) / s.rounds) : 0;
-  return s;
-}
-
-int lane_group_log2(int dim) {
-  int g = 0;
-  while ((8 << g) < dim && g < 6) ++g;
-  return g;
-}
-
-// Tokens per chunk.
-int chunk_tokens(int64_t n, int dim) {
-  (void)n;
-  (void)dim;
-  return 16;
-}
-
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-struct Layout {
-  SortPlan s;
-  int chunk;
-  int64_t chunks;
-  int64_t key[2], pos[2], hist, head, tail, total;  // byte offsets
-};
-
-Layout plan_layout(int64_t n, int64_t rows, int dim) {
-  Layout l;
-  l.s = plan_sort(n, rows);
-  l.chunk = chunk_tokens(n, dim);
-  l.chunks = (n + l.chunk - 1) / l.chunk;
-  int64_t at = 0;
-  auto take = [&](int64_t bytes) {
-    const int64_t o = at;
-    at += round_up(bytes, 256);
-    return o;
-  };
-  for (int i = 0; i < 2; ++i) {
-    l.key[i] = take(n * 4);
-    l.pos[i] = take(n * 4);
+// The value of lane (lane ^ X); every lane is active.
+template <int X>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+  const int i = (int)v;
+  if constexpr (X == 1) {          // quad_perm [1,0,3,2]
+    return __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, true);
+  } else if constexpr (X == 2) {   // quad_perm [2,3,0,1]
+    return __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, true);
+  } else if constexpr (X == 3) {   // quad_perm [3,2,1,0]
+    return __builtin_amdgcn_update_dpp(0, i, 0x1B, 0xF, 0xF, true);
+  } else if constexpr (X == 4) {
+    return lane_xor<3>(lane_xor<7>(v));
+  } else if constexpr (X == 7) {   // mirror of 8 lanes
+    return __builtin_amdgcn_update_dpp(0, i, 0x141, 0xF, 0xF, true);
+  } else if constexpr (X == 8) {   // rotation of 16 lanes by 8
+    return __builtin_amdgcn_update_dpp(0, i, 0x128, 0xF, 0xF, true);
+  } else if constexpr (X == 15) {  // mirror of 16 lanes
+    return __builtin_amdgcn_update_dpp(0, i, 0x140, 0xF, 0xF, true);
+  } else if constexpr (X == 16) {
+    // the swap leaves the lower rows' values in one result, the upper in the other
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return threadIdx.x & 16 ? r[0] : r[1];
+  } else if constexpr (X == 31) {
+    return lane_xor<16>(lane_xor<15>(v));
+  } else if constexpr (X == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return threadIdx.x & 32 ? r[0] : r[1];
+  } else {
+    static_assert(X == 63);
+    return lane_xor<32>(lane_xor<31>(v));
   }
-  l.hist = take(((int64_t)4 << l.s.digit) * l.s.tiles);
-  l.head = take(l.chunks * dim * 4);
-  l.tail = take(l.chunks * dim * 4);
-  l.total = at;
-  return l;
 }
+template <int X>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+  return (uint64_t)lane_xor<X>((uint32_t)(v >> 32)) << 32 | lane_xor<X>((uint32_t)v);
+}
+
+// The lower of two values, or the upper.
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t b, bool low) {
+  const uint32_t x = a < b ? a : b, y = a < b ? b : a;
+  return low ? x : y;
+}
+__device__ __forceinline__ uint64_t pick(uint64_t a, uint64_t b, bool low) {
+  return (a < b) == low ? a : b;
+}
+
+// Puts v[a], v[b] of a thread in order.
+template <typename K>
+__device__ __forceinline__ void in_order(K &a, K &b) {
+  const K x = a < b ? a : b, y = a < b ? b : a;
+  a = x;
+  b = y;
+}
+
+// Steps at distances within a thread: H, H / 2, ..., 1.
+template <int H, typename K, int E>
+__device__ __forceinline__ void thread_steps(K (&v)[E]) {
+  if constexpr (H > 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((e & H) == 0) in_order(v[e], v[e + H]);
+    thread_steps<H / 2>(v);
+  }
+}
+
+// Sorts the values of a thread.
+template <int N, typename K, int E>
+__device__ __forceinline__ void thread_levels(K (&v)[E]) {
+  if constexpr (N <= E) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((e & (N / 2)) == 0) in_order(v[e], v[e ^ (N - 1)]);
+    thread_steps<N / 4>(v);
+    thread_levels<N * 2>(v);
+  }
+}
+
+// Steps at a distance of LANES lanes, of LANES / 2, and so on down to 1 value.
+template <int LANES, typename K, int E>
+__device__ __forceinline__ void close_steps(K (&v)[E]) {
+  if constexpr (LANES > 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      v[e] = pick(v[e], lane_xor<LANES>(v[e]), (threadIdx.x & LANES) == 0);
+    close_steps<LANES / 2>(v);
+  } else {
+    thread_steps<E / 2>(v);
+  }
+}
+
+// Merges sorted runs of LANES / 2 lanes, and so on up to a whole wave.
+template <int LANES, typename K, int E>
+__device__ __forceinline__ void wave_levels(K (&v)[E]) {
+  K o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = lane_xor<LANES - 1>(v[E - 1 - e]);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = pick(v[e], o[e], (threadIdx.x & (LANES / 2)) == 0);
+  close_steps<LANES / 4>(v);
+  if constexpr (LANES < kWave) wave_levels<LANES * 2>(v);
+}
+
+// Sort of P values (a power of two, at least 64 E) by the workgroup: thread t
+// holds values [t E, t E + E) before and after.  A sorting network: a level
+// joins pairs of sorted runs by comparing each value with its mirror image in
+// the pair, then at half the distance and so on, the lower value always to the
+// lower place.  (With that order a step is a move between lanes, a minimum, a
+// maximum and a choice by a constant lane mask; instructions bound it.)  The
+// more values a thread holds, the more of the steps lie within a thread, where
+// they take no move and no choice.  Longer distances than a wave go through
+// two LDS buffers in turn, one barrier each.  `lds` holds 2 P values.
+template <typename K, int E>
+__device__ void block_sort(K (&v)[E], K *lds, int P) {
+  const int first = threadIdx.x * E;
+  const bool there = first < P;
+  if (there) {
+    thread_levels<2>(v);
+    wave_levels<2>(v);
+  }
+  int buf = 0;
+  for (int k = 2 * kWave * E; k <= P; k <<= 1) {
+    for (int half = k >> 1; half >= kWave * E; half >>= 1) {
+      const bool mirror = 2 * half == k;
+      K *b = lds + buf * P;
+      buf ^= 1;
+      if (there) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) b[first + e] = v[e];
+      }
+      __syncthreads();
+      if (there) {  // a thread's partners are the values of one thread
+        const K *q = b + (first ^ (mirror ? k - E : half));
+        K o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = q[e];
+        const bool low = (first & half) == 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = pick(v[e], mirror ? o[E - 1 - e] : o[e], low);
+      }
+    }
+    if (there) close_steps<kWave / 2>(v);
+  }
+}
+
+// What is sorted: the row in the upper bits, the token's index within the
+// tile in the lower ones.  32 bits where both fit, else 64.
+template <typename K, int E>
+__host__ __device__ constexpr int index_bits() {
+  return sizeof(K) == 8 ? 32 : (E == kFew ? 10 : 11);
+}
+
+template <int E>
+constexpr int64_t kRows32 = (int64_t)1 << (32 - index_bits<uint32_t, E>());  // table rows below it
+
+__device__ __forceinline__ uint32_t row_of(int32_t token, int64_t rows) {
+  return token >= 0 && token < rows ? (uint32_t)token : (uint32_t)rows;  // rows: not there
+}
+
+// Values [first, first + E) of the tile of n tokens at `token`; all ones past
+// its end.
+template <typename K, int E>
+__device__ __forceinline__ void load_tile(const int32_t *token, int n, int64_t rows, K (&v)[E]) {
+  const int first = threadIdx.x * E;
+  int32_t t[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) t[e] = first + e < n ? token[first + e] : -1;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    v[e] = first + e < n
+               ? (K)row_of(t[e], rows) << index_bits<K, E>() | (K)(uint32_t)(first + e)
+               : ~(K)0;
+}
+
+// ------------------------------------------------------------------ fill --
 
 // A part of out to be filled with zeros: rows [first, first + count) of
 // `width` elements each (a dense out is one row of all its elements).
@@ -110,208 +239,30 @@ struct Fill {
   int blocks;
 };
 
-__device__ void fill_part(const Fill &f, int block) {
+// `t` of `threads` threads write zeros to a run of bytes, 16 at a time.
+__device__ __forceinline__ void zero_run(uint8_t *p, int64_t bytes, int64_t t, int64_t threads) {
   const u32x4_t zero = {0, 0, 0, 0};
+  const int64_t whole = bytes / 16;
+  for (int64_t i = t; i < whole; i += threads) put16<true>(p + i * 16, zero);
+  for (int64_t i = whole * 16 + t; i < bytes; i += threads) p[i] = 0;
+}
+
+__device__ void fill_part(const Fill &f, int block) {
   if (f.count == 1) {  // dense: one run of bytes
-    uint8_t *p = (uint8_t *)f.out + f.first * f.bytes;
-    const int64_t bytes = f.width * f.bytes;
-    const int64_t whole = bytes / 16;
-    for (int64_t i = (int64_t)block * kSortThreads + threadIdx.x; i < whole;
-         i += (int64_t)f.blocks * kSortThreads)
-      put16<true>(p + i * 16, zero);
-    if (block == 0)
-      for (int64_t i = whole * 16 + threadIdx.x; i < bytes; i += kSortThreads) p[i] = 0;
+    zero_run((uint8_t *)f.out + f.first * f.bytes, f.width * f.bytes,
+             (int64_t)block * blockDim.x + threadIdx.x, (int64_t)f.blocks * blockDim.x);
     return;
   }
-  for (int64_t r = block; r < f.count; r += f.blocks) {
-    uint8_t *p = (uint8_t *)f.out + (f.first + r) * f.ld * f.bytes;
-    const int64_t bytes = f.width * f.bytes;
-    const int64_t whole = bytes / 16;
-    for (int64_t i = threadIdx.x; i < whole; i += kSortThreads) put16<true>(p + i * 16, zero);
-    for (int64_t i = whole * 16 + threadIdx.x; i < bytes; i += kSortThreads) p[i] = 0;
-  }
+  for (int64_t r = block; r < f.count; r += f.blocks)
+    zero_run((uint8_t *)f.out + (f.first + r) * f.ld * f.bytes, f.width * f.bytes, threadIdx.x,
+             blockDim.x);
 }
 
-struct SortPass {
-  int64_t n;
-  const int32_t *key_in, *pos_in;  // pos_in null: the first pass, positions are indices
-  int32_t *key_out, *pos_out;
-  uint32_t *hist;                  // [bin][tile]
-  int32_t rows;
-  int shift, digit, tiles, rounds;
-};
-
-__device__ __forceinline__ uint32_t sort_key(const SortPass &p, int64_t i) {
-  const int32_t k = p.key_in[i];
-  return p.pos_in ? (uint32_t)k : (k >= 0 && k < p.rows ? (uint32_t)k : (uint32_t)p.rows);
-}
-
-// Counts of each digit in each tile of tokens.
-__global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(SortPass p, Fill fill) {
-  extern __shared__ uint32_t lds[];
-  if ((int)blockIdx.x >= p.tiles) {
-    fill_part(fill, blockIdx.x - p.tiles);
-    return;
-  }
-  const int bins = 1 << p.digit;
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) lds[b] = 0;
-  __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * p.rounds * kTile;
-  for (int r = 0; r < p.rounds; ++r) {
-#pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      const int64_t i = first + (int64_t)r * kTile + j * kSortThreads + threadIdx.x;
-      if (i < p.n) atomicAdd(&lds[(sort_key(p, i) >> p.shift) & (bins - 1)], 1u);
-    }
-  }
-  __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortThreads)
-    p.hist[(int64_t)b * p.tiles + blockIdx.x] = lds[b];
-}
-
-// Exclusive scan of one value per thread over the workgroup.
-__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *wave_sums) {
-  uint32_t inc = v;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint32_t u = __shfl_up(inc, o);
-    if ((int)(threadIdx.x % kWave) >= o) inc += u;
-  }
-  if (threadIdx.x % kWave == kWave - 1) wave_sums[threadIdx.x / kWave] = inc;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < (int)(threadIdx.x / kWave); ++w) before += wave_sums[w];
-  __syncthreads();
-  return before + inc - v;
-}
-
-// Moves a tile's tokens to their places.  Equal digits keep their order:
-// a wave takes 256 consecutive tokens, 64 at a time; a lane's rank among
-// equal digits is what its wave has counted before plus the lower lanes with
-// the same digit, found by one ballot per digit bit.
-__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortPass p, Fill fill) {
-  extern __shared__ uint32_t lds[];
-  if ((int)blockIdx.x >= p.tiles) {
-    fill_part(fill, blockIdx.x - p.tiles);
-    return;
-  }
-  const int bins = 1 << p.digit;
-  __shared__ uint32_t wave_sums[kSortWaves];
-  uint32_t *base = lds;                                            // [bins]
-  uint16_t *count = reinterpret_cast<uint16_t *>(lds + bins);      // [waves][bins]
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  for (int b = tid; b < bins * kSortWaves / 2; b += kSortThreads)
-    reinterpret_cast<uint32_t *>(count)[b] = 0;
-
-  // first place of each digit's tokens of this tile
-  const int per = bins > kSortThreads ? bins / kSortThreads : 1;
-  uint32_t mine = 0;
-  for (int k = 0; k < per; ++k) {
-    const int b = tid * per + k;
-    if (b < bins) {
-      const uint32_t *h = p.hist + (int64_t)b * p.tiles;
-      uint32_t all = 0, before = 0;
-      for (int t = 0; t < p.tiles; ++t) {
-        const uint32_t c = h[t];
-        before += t < (int)blockIdx.x ? c : 0;
-        all += c;
-      }
-      base[b] = mine + before;
-      mine += all;
-    }
-  }
-  const uint32_t start = block_exclusive(mine, wave_sums);
-  for (int k = 0; k < per; ++k) {
-    const int b = tid * per + k;
-    if (b < bins) base[b] += start;
-  }
-
-  uint16_t *mine_count = count + wave * bins;
-  for (int r = 0; r < p.rounds; ++r) {
-    __syncthreads();  // counts are zero, base is this round's
-    const int64_t t0 =
-        ((int64_t)blockIdx.x * p.rounds + r) * kTile + wave * (kItems * kWave);
-    // ranks within the wave
-    uint32_t key[kItems], rank[kItems];
-#pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      const int64_t i = t0 + j * kWave + lane;
-      key[j] = i < p.n ? sort_key(p, i) : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      const bool there = t0 + j * kWave + lane < p.n;
-      const uint32_t d = (key[j] >> p.shift) & (bins - 1);
-      uint64_t same = __ballot(there);
-      for (int b = 0; b < p.digit; ++b) {
-        const uint64_t set = __ballot((d >> b) & 1);
-        same &= (d >> b) & 1 ? set : ~set;
-      }
-      const uint32_t lower = __popcll(same & ((1ull << lane) - 1));
-      const uint32_t seen = there ? mine_count[d] : 0;
-      rank[j] = seen + lower;
-      // the wave's LDS accesses are in order: every lane has read the count
-      // before its first lane of this digit raises it
-      __builtin_amdgcn_wave_barrier();
-      if (there && lower == 0) mine_count[d] = (uint16_t)(seen + __popcll(same));
-      __builtin_amdgcn_wave_barrier();
-    }
-    __syncthreads();
-    // what the waves before hold of each digit
-    uint32_t total[(1 << kMaxDigit) / kSortThreads];
-#pragma unroll
-    for (int q = 0; q < (1 << kMaxDigit) / kSortThreads; ++q) {
-      const int b = tid + q * kSortThreads;
-      uint32_t run = 0;
-      if (b < bins) {
-#pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
-          const uint32_t c = count[w * bins + b];
-          count[w * bins + b] = (uint16_t)run;
-          run += c;
-        }
-      }
-      total[q] = run;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      const int64_t i = t0 + j * kWave + lane;
-      if (i < p.n) {
-        const uint32_t d = (key[j] >> p.shift) & (bins - 1);
-        const uint32_t to = base[d] + mine_count[d] + rank[j];
-        p.key_out[to] = (int32_t)key[j];
-        p.pos_out[to] = p.pos_in ? p.pos_in[i] : (int32_t)i;
-      }
-    }
-    if (r + 1 < p.rounds) {
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < (1 << kMaxDigit) / kSortThreads; ++q) {
-        const int b = tid + q * kSortThreads;
-        if (b < bins) {
-          base[b] += total[q];
-#pragma unroll
-          for (int w = 0; w < kSortWaves; ++w) count[w * bins + b] = 0;
-        }
-      }
-    }
-  }
-}
-
-struct ReduceParams {
-  GradParams g;
-  const int32_t *key, *pos;  // sorted
-  float *head, *tail;        // partial sums, one row of dim each per chunk
-  int64_t chunks;
-  int chunk;                 // tokens per chunk
-  int log2g;                 // lanes per group
-  int slices;                // column slices of 8 << log2g
-};
+// ---------------------------------------------------------------- reduce --
 
 // Finishes a row: scale, earlier value, one rounding.
 template <typename TO>
-__device__ __forceinline__ void finish_row(const GradParams &g, int32_t row, int c,
+__device__ __forceinline__ void finish_row(const GradParams &g, uint32_t row, int c,
                                            const float (&acc)[8]) {
   using SO = typename TO::S;
   SO *o = (SO *)g.out + (int64_t)row * g.ld_out;
@@ -327,177 +278,530 @@ __device__ __forceinline__ void finish_row(const GradParams &g, int32_t row, int
   store_chunk<TO>(o, c, g.dim, v);
 }
 
-template <typename TG, typename TO>
-__global__ __launch_bounds__(256) void grad_reduce_kernel(ReduceParams p) {
+// A lane group: the lanes that hold one row of a column slice, 8 elements each.
+struct Lanes {
+  int group, groups;  // of the workgroup
+  int log2g;          // log2 of its lanes
+  int c;              // first column of this lane
+  bool live;          // c < dim
+};
+
+__device__ __forceinline__ Lanes lanes_of(int log2g, int64_t slice, int dim) {
+  const int G = 1 << log2g;
+  Lanes l;
+  l.log2g = log2g;
+  l.group = threadIdx.x >> log2g;
+  l.groups = blockDim.x >> log2g;
+  const int64_t c = (slice * G + (threadIdx.x & (G - 1))) * 8;
+  l.live = c < dim;
+  l.c = l.live ? (int)c : 0;
+  return l;
+}
+
+// Adds up the sorted tokens [t0, t1) by the workgroup, PER (or fewer at the
+// end) for each lane group.  A row that lies in one group's tokens is finished
+// there.  What a group holds of a row that began before it, its head, is
+// added to the group in which the row begins: within a wave by a scan over its
+// groups (a frequent row's tokens fill many groups, and a step by step walk
+// over them took longer than their loads), from wave to wave through `heads`
+// in LDS (two arrays of one float4 per thread).
+//   key(i), pos(i)   row and position of sorted token i
+//   open             the row of t0 began before it: group 0 takes it up from
+//                    what begin(acc) gives
+//   goes_on          the row of t1 - 1 goes on after it: end(acc, began) takes
+//                    its sum so far (began: in this call)
+//   done(row, acc)   takes a finished row
+template <typename TG, int PER, typename Key, typename Pos, typename Begin, typename End,
+          typename Done>
+__device__ __forceinline__ void reduce_tokens(const GradParams &g, const Lanes &l, int t0, int t1,
+                                              bool open, bool goes_on, f32x4_t *heads,
+                                              Key key, Pos pos, Begin begin, End end, Done done) {
   using SG = typename TG::S;
-  const int G = 1 << p.log2g;
-  const int lane = threadIdx.x & (G - 1);
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> p.log2g;
-  const int64_t chunk = item / p.slices;
-  if (chunk >= p.chunks) return;
-  const int c = ((int)(item - chunk * p.slices) * G + lane) * 8;
-  if (c >= p.g.dim) return;
-  const int32_t rows = (int32_t)p.g.rows;
-  const int64_t s0 = chunk * p.chunk;
-  const int64_t s1 = s0 + p.chunk < p.g.n ? s0 + p.chunk : p.g.n;
-  const int32_t before = s0 > 0 ? p.key[s0 - 1] : -1;
-  float acc[8];
+  const int a = t0 + l.group * PER;
+  const int b = a + PER < t1 ? a + PER : t1;
+  float acc[8], head[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-  bool fresh = true;  // the running row began in this chunk
-  for (int64_t s = s0; s < s1; s += kUnroll) {
-    int32_t key[kUnroll + 1];
-    float v[kUnroll][8];
+  for (int e = 0; e < 8; ++e) acc[e] = head[e] = 0.0f;
+  bool tail = false;  // acc holds a row that begins here and goes on
+  bool pass = false;  // head holds all tokens of the group, and their row goes on
+  if (l.live && a < b) {
+    Chunk<TG> v[PER];
 #pragma unroll
-    for (int j = 0; j <= kUnroll; ++j) key[j] = s + j < p.g.n ? p.key[s + j] : rows;
+    for (int j = 0; j < PER; ++j)
+      if (a + j < b) v[j].load((const SG *)g.grad + (int64_t)pos(a + j) * g.ld_grad, l.c, g.dim);
+    bool fresh = a == t0 ? !open : key(a - 1) != key(a);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      // (positions of the chunk only: a chunk is a multiple of kUnroll)
-      if (key[j] < rows) {
-        load_chunk<TG>((const SG *)p.g.grad + (int64_t)p.pos[s + j] * p.g.ld_grad, c, p.g.dim,
-                       v[j]);
-      } else {
+    for (int j = 0; j < PER; ++j) {
+      if (a + j < b) {
+        const uint32_t row = key(a + j);
+        const bool more = a + j + 1 < t1 ? key(a + j + 1) == row : goes_on;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
-      }
-    }
-    if (s == s0) fresh = before != key[0];
+        for (int e = 0; e < 8; ++e) acc[e] += v[j].at(e);
+        if (!more || a + j + 1 == b) {
+          if (!fresh) {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      if (key[j] >= rows) return;  // only tokens outside the table follow
+            for (int e = 0; e < 8; ++e) head[e] = acc[e];
+            pass = more;
+          } else if (more) {
+            tail = true;
+          } else {
+            done(row, acc);
+          }
+          fresh = true;
+          if (!tail) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[j][e];
-      const bool more = key[j + 1] == key[j];
-      const bool border = s + j + 1 == s1;
-      if (!more || border) {
-        if (!fresh)
-          store_chunk<F32>(p.head + chunk * p.g.dim, c, p.g.dim, acc);
-        else if (more)
-          store_chunk<F32>(p.tail + chunk * p.g.dim, c, p.g.dim, acc);
-        else
-          finish_row<TO>(p.g, key[j], c, acc);
-        fresh = true;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-      }
-    }
-  }
-}
-
-// Whether a row's tokens begin in `chunk` and go on in the next one.
-__device__ __forceinline__ bool crosses(const ReduceParams &p, int64_t chunk, int32_t &key) {
-  const int64_t s1 = (chunk + 1) * p.chunk;
-  if (s1 >= p.g.n) return false;
-  key = p.key[s1 - 1];
-  if (key >= p.g.rows || p.key[s1] != key) return false;
-  const int64_t s0 = chunk * p.chunk;
-  return p.key[s0] != key || s0 == 0 || p.key[s0 - 1] != key;
-}
-
-// How many chunks after `chunk` a crossing row reaches, counted up to limit.
-__device__ __forceinline__ int parts_after(const ReduceParams &p, int64_t chunk, int32_t key,
-                                           int limit) {
-  int n = 0;
-  for (int k = 1; k <= limit; ++k) {
-    const int64_t s = (chunk + k) * p.chunk;
-    n += s < p.g.n && p.key[s] == key ? 1 : 0;
-  }
-  return n;
-}
-
-// Adds the partial sums of rows that cross chunks.  A workgroup looks at as
-// many chunks as it has lane groups.  A row of few chunks is added by its
-// lane group; a longer one by the whole workgroup, each lane group a run of
-// its partials, the runs' sums in order through LDS.
-template <typename TO>
-__global__ __launch_bounds__(kFixThreads) void grad_fix_kernel(ReduceParams p) {
-  const int G = 1 << p.log2g, NG = kFixThreads >> p.log2g;
-  const int lane = threadIdx.x & (G - 1), group = threadIdx.x >> p.log2g;
-  const int slice = blockIdx.y;
-  const int c = (slice * G + lane) * 8;
-  const bool live = c < p.g.dim;
-  const int64_t first = (int64_t)blockIdx.x * NG;
-  __shared__ int nlong;
-  __shared__ int64_t longs[kFixThreads];
-  __shared__ float sums[kFixThreads][8];
-  if (threadIdx.x == 0) nlong = 0;
-  __syncthreads();
-  {
-    const int64_t chunk = first + group;
-    int32_t key = 0;
-    if (chunk < p.chunks && crosses(p, chunk, key)) {
-      const int n = parts_after(p, chunk, key, kShortParts + 1);
-      if (n <= kShortParts) {
-        if (live) {
-          float acc[8], v[kShortParts][8];
-          load_chunk<F32>(p.tail + chunk * p.g.dim, c, p.g.dim, acc);
-#pragma unroll
-          for (int k = 0; k < kShortParts; ++k)
-            if (k < n) load_chunk<F32>(p.head + (chunk + 1 + k) * p.g.dim, c, p.g.dim, v[k]);
-#pragma unroll
-          for (int k = 0; k < kShortParts; ++k)
-            if (k < n)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) acc[e] += v[k][e];
-          finish_row<TO>(p.g, key, c, acc);
+            for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+          }
         }
-      } else if (lane == 0) {
-        longs[atomicAdd(&nlong, 1)] = chunk;
       }
     }
   }
+  // head: the group's and, where its row goes on, those of the wave's groups
+  // after it, as far as the row reaches
+  const int G = 1 << l.log2g, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  for (int d = G; d < kWave; d <<= 1) {
+    const bool next = __shfl_down((int)pass, d);
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __shfl_down(head[e], d);
+    if (pass && lane + d < kWave) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) head[e] += o[e];
+      pass = next;
+    }
+  }
+  if (G < kWave) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float o = __shfl_down(head[e], G);
+      if (tail && lane + G < kWave) acc[e] += o;
+    }
+  }
+  f32x4_t *head_lo = heads, *head_hi = heads + blockDim.x;
+  if (lane < G) {
+    head_lo[wave * G + lane] = f32x4_t{head[0], head[1], head[2], head[3]};
+    head_hi[wave * G + lane] = f32x4_t{head[4], head[5], head[6], head[7]};
+  }
   __syncthreads();
-  const int todo = nlong;
-  for (int w = 0; w < todo; ++w) {
-    const int64_t chunk = longs[w];
-    const int32_t key = p.key[(chunk + 1) * p.chunk - 1];
-    int64_t n = 0;  // chunks after this one that the row reaches
+  // adds the heads of the waves after this one that the row reaches
+  auto walk = [&](uint32_t row, bool began) {
+    const int stride = (kWave >> l.log2g) * PER;
+    int w = wave + 1;
+    for (int s = t0 + w * stride; s < t1 && key(s) == row; s += stride, ++w) {
+      const f32x4_t lo = head_lo[w * G + lane % G], hi = head_hi[w * G + lane % G];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[e] += lo[e];
+        acc[4 + e] += hi[e];
+      }
+    }
+    if (goes_on && key(t1 - 1) == row)
+      end(acc, began);
+    else
+      done(row, acc);
+  };
+  if (tail) walk(key(b - 1), true);
+  if (open && l.group == 0 && l.live && t0 < t1) {
+    begin(acc);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += head[e];
+    walk(key(t0), false);
+  }
+}
+
+// ------------------------------------------------------------ one launch --
+
+struct SmallParams {
+  GradParams g;
+  int P;         // power of two that holds the tokens
+  int segments;  // parts of the sorted order
+  int slices;    // column slices of 8 << log2g
+  int log2g;
+};
+
+// Zeros for those of rows [r0, r1) that no token names, by one workgroup: a
+// bitmap of the rows in LDS (kBitmap bits), one mark for each token.
+constexpr int kBitmap = 1 << 16;
+template <int BYTES>
+__device__ void fill_unnamed(const GradParams &g, int64_t r0, int64_t r1, uint32_t *bits) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int64_t row_bytes = (int64_t)g.dim * BYTES, ld_bytes = g.ld_out * BYTES;
+  int share = 0;  // log2 of the lanes that share a row
+  while (share < 6 && (16 << share) < row_bytes) ++share;
+  for (int64_t q0 = r0; q0 < r1; q0 += kBitmap) {
+    const int count = r1 - q0 < kBitmap ? (int)(r1 - q0) : kBitmap;
+    for (int i = threadIdx.x; i < (count + 31) / 32; i += kThreads) bits[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < (int)g.n; i += kThreads) {
+      const int64_t r = g.token[i] - q0;  // (a token outside the table is outside [q0, r1))
+      if (r >= 0 && r < count) atomicOr(&bits[r >> 5], 1u << (r & 31));
+    }
+    __syncthreads();
+    const int each = (count + kWaves - 1) / kWaves < kWave ? (count + kWaves - 1) / kWaves : kWave;
+    for (int r = wave * each; r < count; r += kWaves * each) {
+      const int rows = count - r < each ? count - r : each;
+      const bool named = lane < rows && (bits[(r + lane) >> 5] >> ((r + lane) & 31) & 1);
+      const uint64_t mask = __ballot(named);
+      uint8_t *o = (uint8_t *)g.out + (q0 + r) * ld_bytes;
+      if (mask == 0 && ld_bytes == row_bytes) {
+        zero_run(o, rows * row_bytes, lane, kWave);
+      } else {
+        for (int q = lane >> share; q < rows; q += kWave >> share)
+          if (!((mask >> q) & 1))
+            zero_run(o + q * ld_bytes, row_bytes, lane & ((1 << share) - 1), 1 << share);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename TG, typename TO, typename K, int E>
+__global__ __launch_bounds__(kThreads) void small_kernel(SmallParams p) {
+  constexpr int B = index_bits<K, E>();
+  __shared__ K sorted[2 * kThreads * E];
+  __shared__ f32x4_t heads[2 * kThreads];
+  __shared__ f32x4_t carry[2][2][kWave];  // the open row's sum, by round parity
+  const GradParams &g = p.g;
+  const int n = (int)g.n;
+  if ((int)blockIdx.x >= p.segments * p.slices) {
+    const int blocks = gridDim.x - p.segments * p.slices;
+    const int64_t b = blockIdx.x - p.segments * p.slices;
+    fill_unnamed<sizeof(typename TO::S)>(g, g.rows * b / blocks, g.rows * (b + 1) / blocks,
+                                         (uint32_t *)sorted);
+    return;
+  }
+  K v[E];
+  load_tile<K, E>(g.token, n, g.rows, v);
+  int nv = 0;  // tokens in the table
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    nv += __syncthreads_count((uint64_t)(v[e] >> B) < (uint64_t)g.rows ? 1 : 0);
+  block_sort<K, E>(v, sorted, p.P);
+  __syncthreads();
+  if ((int)threadIdx.x * E < p.P) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sorted[threadIdx.x * E + e] = v[e];
+  }
+  __syncthreads();
+  auto key = [&](int i) { return (uint32_t)(sorted[i] >> B); };
+  auto pos = [&](int i) { return (uint32_t)sorted[i] & (uint32_t)(((uint64_t)1 << B) - 1); };
+  // the first sorted token whose row is not below `row`
+  auto place = [&](uint32_t row) {
+    int at = 0;
+    for (int s = p.P >> 1; s > 0; s >>= 1)
+      if (at + s <= nv && key(at + s - 1) < row) at += s;
+    return at + (at < nv && key(at) < row ? 1 : 0);
+  };
+
+  const Lanes l = lanes_of(p.log2g, blockIdx.x % p.slices, g.dim);
+  const int seg = blockIdx.x / p.slices;
+  const int len = (nv + p.segments - 1) / p.segments;
+  // a segment owns the rows that begin in it, to their last token
+  auto border = [&](int s) {
+    if (s >= nv) return nv;
+    if (s > 0 && key(s - 1) == key(s)) return place(key(s) + 1);
+    return s;
+  };
+  const int start = border(seg * len), stop = border((seg + 1) * len);
+  const int lane = threadIdx.x & ((1 << p.log2g) - 1);
+  auto add_up = [&](auto per) {
+    constexpr int PER = decltype(per)::value;
+    int round = 0;
+    for (int t0 = start; t0 < stop; t0 += l.groups * PER, round ^= 1) {
+      const int t1 = t0 + l.groups * PER < stop ? t0 + l.groups * PER : stop;
+      reduce_tokens<TG, PER>(
+          g, l, t0, t1, t0 > start && key(t0 - 1) == key(t0),
+          t1 < stop && key(t1 - 1) == key(t1), heads, key, pos,
+          [&](float (&acc)[8]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[e] = carry[round][0][lane][e];
+              acc[4 + e] = carry[round][1][lane][e];
+            }
+          },
+          [&](const float (&acc)[8], bool) {
+            carry[round ^ 1][0][lane] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+            carry[round ^ 1][1][lane] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
+          },
+          [&](uint32_t row, const float (&acc)[8]) { finish_row<TO>(g, row, l.c, acc); });
+      __syncthreads();  // heads are read before the next round writes them
+    }
+  };
+  // a token for each lane group where that is one round, else eight
+  if (stop - start <= l.groups)
+    add_up(std::integral_constant<int, 1>());
+  else
+    add_up(std::integral_constant<int, kMaxPer>());
+}
+
+// --------------------------------------------------------- sorting tokens --
+
+template <typename K>
+__global__ __launch_bounds__(kThreads) void tile_sort_kernel(const int32_t *token, int64_t n,
+                                                             int64_t rows, int tiles, int32_t *key,
+                                                             int32_t *pos, Fill fill) {
+  constexpr int E = kMany, B = index_bits<K, E>();
+  if ((int)blockIdx.x >= tiles) {
+    fill_part(fill, blockIdx.x - tiles);
+    return;
+  }
+  __shared__ K lds[2 * kTile];
+  const int64_t base = (int64_t)blockIdx.x * kTile;
+  const int count = n - base < kTile ? (int)(n - base) : kTile;
+  K v[E];
+  load_tile<K, E>(token + base, count, rows, v);
+  block_sort<K, E>(v, lds, kTile);
+  const int first = threadIdx.x * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (first + e < count) {
+      key[base + first + e] = (int32_t)(v[e] >> B);
+      pos[base + first + e] =
+          (int32_t)(base + ((uint32_t)v[e] & (uint32_t)(((uint64_t)1 << B) - 1)));
+    }
+  }
+}
+
+struct MergeParams {
+  int64_t n, run;  // tokens, length of a sorted run (the last may be shorter)
+  int fan;         // runs that make one
+  const int32_t *key_in, *pos_in;
+  int32_t *key_out, *pos_out;
+  int64_t blocks;  // of tokens
+};
+
+// A workgroup places 64 neighbouring tokens of one run: each of its waves
+// searches for them in every kMergeWaves-th run, kSearches runs at a time, so
+// that few steps wait for one another, and the waves' counts are added.
+__global__ __launch_bounds__(kMergeThreads) void merge_kernel(MergeParams p, Fill fill) {
+  if ((int64_t)blockIdx.x >= p.blocks) {
+    fill_part(fill, (int)(blockIdx.x - p.blocks));
+    return;
+  }
+  __shared__ int32_t counts[kMergeWaves][kWave];
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t i0 = (int64_t)blockIdx.x * kWave;  // (a run is a multiple of 64)
+  const bool there = i0 + lane < p.n;
+  const int64_t run = p.run, span = run * p.fan;
+  const int64_t base = i0 / span * span;
+  const int mine = (int)((i0 - base) / run);
+  const int32_t key = there ? p.key_in[i0 + lane] : 0;
+  const int64_t left = (p.n - base + run - 1) / run;
+  const int fan = left < p.fan ? (int)left : p.fan;
+  uint32_t top = 1;
+  while ((int64_t)top * 2 <= run) top *= 2;
+  uint32_t before = 0;
+  for (int q0 = wave; q0 < fan; q0 += kSearches * kMergeWaves) {
+    // tokens of run q that come before this one: those of lower rows, and in
+    // the runs before its own those of its row too
+    const char *a[kSearches];
+    uint32_t len[kSearches], at[kSearches];
+    int32_t limit[kSearches];
+#pragma unroll
+    for (int u = 0; u < kSearches; ++u) {
+      const int q = q0 + u * kMergeWaves;
+      const bool search = q < fan && q != mine;
+      const int64_t start = base + (search ? q : 0) * run;
+      a[u] = (const char *)(p.key_in + start);
+      len[u] = search ? (uint32_t)(p.n - start < run ? p.n - start : run) : 0;
+      limit[u] = key + (q < mine ? 1 : 0);
+      at[u] = 0;
+    }
+    for (uint32_t s = top; s > 0; s >>= 1) {
+      int32_t got[kSearches];
+#pragma unroll
+      for (int u = 0; u < kSearches; ++u)
+        if (len[u] > 0)  // (index 0: in range, not used)
+          got[u] = *(const int32_t *)(a[u] + (at[u] + s <= len[u] ? at[u] + s - 1 : 0u) * 4u);
+#pragma unroll
+      for (int u = 0; u < kSearches; ++u)
+        if (len[u] > 0) at[u] += at[u] + s <= len[u] && got[u] < limit[u] ? s : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kSearches; ++u) before += at[u];
+  }
+  counts[wave][lane] = (int32_t)before;
+  __syncthreads();
+  if (wave == 0 && there) {
+    int64_t to = i0 + lane - mine * run;  // base and the place in its own run
+#pragma unroll
+    for (int w = 0; w < kMergeWaves; ++w) to += counts[w][lane];
+    p.key_out[to] = key;
+    p.pos_out[to] = p.pos_in[i0 + lane];
+  }
+}
+
+struct ReduceParams {
+  GradParams g;
+  const int32_t *key, *pos;  // sorted
+  float *head, *tail;        // partial sums, one row of dim each per part
+  int64_t parts;
+  int part;                  // tokens per part: lane groups * per
+  int log2g;                 // lanes per group
+  int slices;                // column slices of 8 << log2g
+};
+
+template <typename TG, typename TO, int PER>
+__global__ __launch_bounds__(kReduceThreads) void reduce_kernel(ReduceParams p) {
+  __shared__ uint32_t keys[kReduceThreads * PER + 2];  // from the token before the part on
+  __shared__ uint32_t where[kReduceThreads * PER];
+  __shared__ f32x4_t heads[2 * kReduceThreads];
+  const GradParams &g = p.g;
+  for (int64_t item = blockIdx.x; item < p.parts * p.slices; item += gridDim.x) {
+    const int64_t part = item / p.slices, s0 = part * p.part;
+    const Lanes l = lanes_of(p.log2g, item - part * p.slices, g.dim);
+    int nv = 0;  // tokens of the part that are in the table
+    for (int i = threadIdx.x; i < p.part + 2; i += kReduceThreads) {
+      const int64_t s = s0 + i - 1;
+      keys[i] = s >= 0 && s < g.n ? (uint32_t)p.key[s] : (uint32_t)g.rows;
+      if (i < p.part && s + 1 < g.n) where[i] = (uint32_t)p.pos[s + 1];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i - (int)threadIdx.x < p.part; i += kReduceThreads)
+      nv += __syncthreads_count(i < p.part && keys[1 + (i < p.part ? i : 0)] < (uint32_t)g.rows);
+    if (nv > 0) {
+      const bool open = s0 > 0 && keys[0] == keys[1];
+      const bool goes_on = nv == p.part && keys[nv + 1] == keys[nv];
+      reduce_tokens<TG, PER>(
+          g, l, 0, nv, open, goes_on, heads, [&](int i) { return keys[1 + i]; },
+          [&](int i) { return where[i]; },
+          [&](float (&acc)[8]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+          },
+          [&](const float (&acc)[8], bool began) {
+            store_chunk<F32>((began ? p.tail : p.head) + part * g.dim, l.c, g.dim, acc);
+          },
+          [&](uint32_t row, const float (&acc)[8]) {
+            // a row that began in an earlier part ends here
+            if (open && row == keys[0])
+              store_chunk<F32>(p.head + part * g.dim, l.c, g.dim, acc);
+            else
+              finish_row<TO>(g, row, l.c, acc);
+          });
+    }
+    __syncthreads();  // before the next item's keys
+  }
+}
+
+// Adds the partial sums of a row that crosses parts: the workgroup of the part
+// in which the row begins (the others end at once).  Partial 0 is that part's
+// tail, partial k the head of the k-th part after it.  Each lane group adds a
+// run of them, and the groups' sums are joined in order through LDS.
+template <typename TO>
+__global__ __launch_bounds__(kFixThreads) void fix_kernel(ReduceParams p) {
+  const GradParams &g = p.g;
+  const int G = 1 << p.log2g;
+  const Lanes l = lanes_of(p.log2g, blockIdx.y, g.dim);
+  __shared__ f32x4_t sums[2][kFixThreads];
+  for (int64_t part = blockIdx.x; part < p.parts; part += gridDim.x) {
+    const int64_t s0 = part * p.part, s1 = s0 + p.part;
+    if (s1 >= g.n) return;  // the last part
+    const int32_t row = p.key[s1 - 1];
+    const int32_t next = p.key[s1], first = p.key[s0], before = s0 > 0 ? p.key[s0 - 1] : -1;
+    if (row >= g.rows || next != row || (first == row && before == row)) continue;
+    int64_t n = 0;  // parts after this one that the row reaches
     for (;;) {
-      const int64_t s = (chunk + 1 + n + threadIdx.x) * p.chunk;
-      const int got = __syncthreads_count(s < p.g.n && p.key[s] == key);
+      const int64_t s = s1 + (n + threadIdx.x) * p.part;
+      const int got = __syncthreads_count(s < g.n && p.key[s] == row);
       n += got;
       if (got < kFixThreads) break;
     }
-    // partial 0 is the tail, partial k the head of chunk + k
-    const int64_t per = (n + 1 + NG - 1) / NG;
-    const int64_t k0 = group * per, k1 = k0 + per < n + 1 ? k0 + per : n + 1;
+    const int64_t each = (n + 1 + l.groups - 1) / l.groups;
+    const int64_t k0 = l.group * each, k1 = k0 + each < n + 1 ? k0 + each : n + 1;
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    if (live) {
+    if (l.live) {
       for (int64_t k = k0; k < k1; k += kUnroll) {
         float v[kUnroll][8];
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          if (k + j < k1) {
-            const float *src = k + j == 0 ? p.tail + chunk * p.g.dim
-                                          : p.head + (chunk + k + j) * p.g.dim;
-            load_chunk<F32>(src, c, p.g.dim, v[j]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
-          }
-        }
+        for (int j = 0; j < kUnroll; ++j)
+          if (k + j < k1)
+            load_chunk<F32>((k + j == 0 ? p.tail : p.head) + (part + k + j) * g.dim, l.c, g.dim,
+                            v[j]);
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j)
+          if (k + j < k1)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] += v[j][e];
+            for (int e = 0; e < 8; ++e) acc[e] += v[j][e];
       }
     }
+    // the groups' sums, neighbours first
+    for (int half = 1; half < l.groups && half <= n; half *= 2) {
+      sums[0][threadIdx.x] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+      sums[1][threadIdx.x] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
+      __syncthreads();
+      if (l.group % (2 * half) == 0) {
+        const f32x4_t lo = sums[0][threadIdx.x + half * G], hi = sums[1][threadIdx.x + half * G];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = acc[e];
-    __syncthreads();
-    if (group == 0 && live) {
-      for (int q = 1; q < NG; ++q)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += sums[q * G + lane][e];
-      finish_row<TO>(p.g, key, c, acc);
+        for (int e = 0; e < 4; ++e) {
+          acc[e] += lo[e];
+          acc[4 + e] += hi[e];
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    if (l.group == 0 && l.live) finish_row<TO>(g, (uint32_t)row, l.c, acc);
   }
 }
 
-Fill part_of(const GradParams &g, int out_bytes, int part, int parts) {
+// ---------------------------------------------------------------- launch --
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// log2 of the lanes that hold a row: 8 elements each, up to `most`.
+int lane_group_log2(int dim, int most) {
+  int g = 0;
+  while ((8 << g) < dim && g < most) ++g;
+  return g;
+}
+
+struct Layout {
+  int levels, fan;
+  int log2g, slices, per, part;
+  int64_t parts;
+  int64_t key[2], pos[2], head, tail, total;  // byte offsets
+};
+
+Layout plan_layout(int64_t n, int64_t rows, int dim) {
+  (void)rows;
+  Layout l{};
+  const int64_t tiles = (n + kTile - 1) / kTile;
+  l.levels = tiles <= kOneMerge ? 1 : 0;
+  if (tiles > kOneMerge)
+    for (int64_t all = 1; all < tiles; all *= kMaxFan) ++l.levels;
+  l.fan = 1;
+  for (;; ++l.fan) {  // the least fan whose power reaches all tiles
+    int64_t all = 1;
+    for (int i = 0; i < l.levels; ++i) all *= l.fan;
+    if (all >= tiles) break;
+  }
+  l.log2g = lane_group_log2(dim, 6);
+  l.slices = (dim + (8 << l.log2g) - 1) / (8 << l.log2g);
+  const int groups = kReduceThreads >> l.log2g;
+  l.per = kMaxPer;
+  while (l.per > 2 && n / ((int64_t)groups * l.per) * l.slices < 1024) l.per /= 2;
+  l.part = groups * l.per;
+  l.parts = (n + l.part - 1) / l.part;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  for (int i = 0; i < 2; ++i) {
+    l.key[i] = take(n * 4);
+    l.pos[i] = take(n * 4);
+  }
+  l.head = take(l.parts * dim * 4);
+  l.tail = take(l.parts * dim * 4);
+  l.total = at;
+  return l;
+}
+
+Fill part_of(const GradParams &g, int out_bytes, int part, int parts, int threads) {
   Fill f{};
   f.out = g.out;
   f.ld = g.ld_out;
@@ -510,8 +814,9 @@ Fill part_of(const GradParams &g, int out_bytes, int part, int parts) {
     f.first = a;
     f.count = 1;
     f.width = b - a;
-    const int64_t want = (f.width * out_bytes / 16 + kSortThreads - 1) / kSortThreads;
-    f.blocks = (int)(want < 1 ? 1 : want < kFillBlocks ? want : kFillBlocks);
+    const int64_t want = (f.width * out_bytes / 16 + threads - 1) / threads;
+    const int64_t most = (int64_t)kFillBlocks * kThreads / threads;
+    f.blocks = (int)(want < 1 ? 1 : want < most ? want : most);
   } else {
     const int64_t a = g.rows * part / parts, b = g.rows * (part + 1) / parts;
     f.first = a;
@@ -523,66 +828,101 @@ Fill part_of(const GradParams &g, int out_bytes, int part, int parts) {
   return f;
 }
 
+template <typename TG, typename TO, typename K, int E>
+void launch_small(const GradParams &g, hipStream_t stream) {
+  SmallParams p{};
+  p.g = g;
+  p.P = kWave * E;
+  while (p.P < g.n) p.P *= 2;
+  // 64 columns to a workgroup, and as many parts of the tokens as make 1024
+  // workgroups: all sort the same tokens, so more would only sort more often
+  p.log2g = lane_group_log2(g.dim, 3);
+  while (p.log2g < 6 && (g.dim + (8 << p.log2g) - 1) / (8 << p.log2g) > 64) ++p.log2g;
+  p.slices = (g.dim + (8 << p.log2g) - 1) / (8 << p.log2g);
+  const int groups = kThreads >> p.log2g;
+  const int64_t most = (g.n + groups - 1) / groups, fit = 1024 / p.slices;
+  p.segments = (int)(most < 1 ? 1 : fit < 1 ? 1 : most < fit ? most : fit);
+  int64_t blocks = (int64_t)p.segments * p.slices;
+  if (!g.accumulate) {  // further ones for the rows that no token names
+    int64_t fill = g.rows * g.dim * (int64_t)sizeof(typename TO::S) / (kThreads * 64);
+    if (fill > kFillBlocks) fill = kFillBlocks;
+    if (fill > g.rows) fill = g.rows;
+    blocks += fill < 1 ? 1 : fill;
+  }
+  launch_kernel(small_kernel<TG, TO, K, E>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p);
+}
+
 template <typename TG, typename TO>
 hipError_t launch_typed(const GradParams &g, void *ws, hipStream_t stream) {
+  if (g.n <= kTile) {
+    if (g.n <= kFew * kThreads) {
+      if (g.rows < kRows32<kFew>)
+        launch_small<TG, TO, uint32_t, kFew>(g, stream);
+      else
+        launch_small<TG, TO, uint64_t, kFew>(g, stream);
+    } else if (g.rows < kRows32<kMany>) {
+      launch_small<TG, TO, uint32_t, kMany>(g, stream);
+    } else {
+      launch_small<TG, TO, uint64_t, kMany>(g, stream);
+    }
+    return hipGetLastError();
+  }
   const int ob = (int)sizeof(typename TO::S);
   uint8_t *w = (uint8_t *)ws;
   const Layout l = plan_layout(g.n, g.rows, g.dim);
-  const int parts = g.n > 0 ? 2 * l.s.passes : 1;
-  SortPass sp{};
-  sp.n = g.n;
-  sp.rows = (int32_t)g.rows;
-  sp.digit = l.s.digit;
-  sp.tiles = l.s.tiles;
-  sp.rounds = l.s.rounds;
-  sp.hist = (uint32_t *)(w + l.hist);
-  sp.key_in = g.token;
-  hipError_t e;
-  if (g.n == 0) {  // tiles is 0: the launch only fills
-    const Fill f = part_of(g, ob, 0, 1);
-    if (f.blocks > 0)
-      launch_kernel(sort_hist_kernel, dim3(f.blocks), dim3(kSortThreads), 0, stream, sp, f);
-    return hipGetLastError();
-  }
-  const size_t bins = (size_t)1 << l.s.digit;
-  for (int pass = 0; pass < l.s.passes; ++pass) {
-    sp.shift = pass * l.s.digit;
-    sp.key_out = (int32_t *)(w + l.key[pass & 1]);
-    sp.pos_out = (int32_t *)(w + l.pos[pass & 1]);
-    Fill f = part_of(g, ob, 2 * pass, parts);
-    launch_kernel(sort_hist_kernel, dim3(sp.tiles + f.blocks), dim3(kSortThreads), bins * 4,
-                  stream, sp, f);
-    f = part_of(g, ob, 2 * pass + 1, parts);
-    launch_kernel(sort_scatter_kernel, dim3(sp.tiles + f.blocks), dim3(kSortThreads),
-                  bins * (4 + 2 * kSortWaves), stream, sp, f);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    sp.key_in = sp.key_out;
-    sp.pos_in = sp.pos_out;
+  const int fills = 1 + l.levels;
+  int32_t *key = (int32_t *)(w + l.key[0]), *pos = (int32_t *)(w + l.pos[0]);
+  const int tiles = (int)((g.n + kTile - 1) / kTile);
+  Fill f = part_of(g, ob, 0, fills, kThreads);
+  const dim3 grid((unsigned)(tiles + f.blocks)), block(kThreads);
+  if (g.rows < kRows32<kMany>)
+    launch_kernel(tile_sort_kernel<uint32_t>, grid, block, 0, stream, g.token, g.n, g.rows, tiles,
+                  key, pos, f);
+  else
+    launch_kernel(tile_sort_kernel<uint64_t>, grid, block, 0, stream, g.token, g.n, g.rows, tiles,
+                  key, pos, f);
+  MergeParams m{};
+  m.n = g.n;
+  m.run = kTile;
+  m.fan = l.fan;
+  m.blocks = (g.n + kWave - 1) / kWave;
+  for (int level = 0; level < l.levels; ++level) {
+    m.key_in = (const int32_t *)(w + l.key[level & 1]);
+    m.pos_in = (const int32_t *)(w + l.pos[level & 1]);
+    m.key_out = (int32_t *)(w + l.key[(level + 1) & 1]);
+    m.pos_out = (int32_t *)(w + l.pos[(level + 1) & 1]);
+    f = part_of(g, ob, 1 + level, fills, kMergeThreads);
+    launch_kernel(merge_kernel, dim3((unsigned)(m.blocks + f.blocks)), dim3(kMergeThreads), 0,
+                  stream, m, f);
+    m.run *= l.fan;
   }
   ReduceParams rp{};
   rp.g = g;
-  rp.key = sp.key_in;
-  rp.pos = sp.pos_in;
+  rp.key = (const int32_t *)(w + l.key[l.levels & 1]);
+  rp.pos = (const int32_t *)(w + l.pos[l.levels & 1]);
   rp.head = (float *)(w + l.head);
   rp.tail = (float *)(w + l.tail);
-  rp.chunks = l.chunks;
-  rp.chunk = l.chunk;
-  rp.log2g = lane_group_log2(g.dim);
-  rp.slices = (g.dim + (8 << rp.log2g) - 1) / (8 << rp.log2g);
-  const int64_t lanes = (rp.chunks * rp.slices) << rp.log2g;
-  launch_kernel(grad_reduce_kernel<TG, TO>, dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0,
-                stream, rp);
-  const int ng = kFixThreads >> rp.log2g;
-  launch_kernel(grad_fix_kernel<TO>, dim3((unsigned)((rp.chunks + ng - 1) / ng), rp.slices),
-                dim3(kFixThreads), 0, stream, rp);
+  rp.parts = l.parts;
+  rp.part = l.part;
+  rp.log2g = l.log2g;
+  rp.slices = l.slices;
+  const int64_t items = l.parts * l.slices;
+  const dim3 reduce_grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks));
+  if (l.per == 8)
+    launch_kernel(reduce_kernel<TG, TO, 8>, reduce_grid, dim3(kReduceThreads), 0, stream, rp);
+  else if (l.per == 4)
+    launch_kernel(reduce_kernel<TG, TO, 4>, reduce_grid, dim3(kReduceThreads), 0, stream, rp);
+  else
+    launch_kernel(reduce_kernel<TG, TO, 2>, reduce_grid, dim3(kReduceThreads), 0, stream, rp);
+  const int64_t blocks = l.parts * l.slices < kMaxBlocks ? l.parts : kMaxBlocks / l.slices;
+  launch_kernel(fix_kernel<TO>, dim3((unsigned)blocks, l.slices), dim3(kFixThreads), 0, stream, rp);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t lookup_grad_workspace(int64_t n, int64_t rows, int dim) {
-  return n > 0 ? (size_t)plan_layout(n, rows, dim).total : 0;
+  return n > kTile ? (size_t)plan_layout(n, rows, dim).total : 0;
 }
 
 hipError_t launch_lookup_grad(const GradParams &g, int grad_dtype, int out_dtype, void *ws,

@@ -8,80 +8,110 @@ on the stream the call runs on, and raises on refusal.  There is no CPU path.
 """
 from __future__ import annotations
 
-from .abi import ACTS, _check, _empty, _stream, load
+from .abi import ACTS, _check, _empty, load
 
-_CODES = {}   # torch dtype -> dlrm_dtype, filled on the first call (torch is imported late)
+# One call of a short operator is as long as its marshalling, so each tensor's
+# shape and strides are read once, the device is asked for once a call, and the
+# current stream is taken as the raw handle that the C entry point wants.
+_CODES = {}    # torch dtype -> dlrm_dtype, filled on the first call (torch is imported late)
+_MODULE = None
+_FLOATS = ()   # float32, bfloat16
+_TABLES = ()   # and the table's FP8
+_INT8 = ()
 
 
 def _torch():
-    import torch
-    if not _CODES:
+    global _MODULE, _FLOATS, _TABLES, _INT8
+    if _MODULE is None:
+        import torch
         _CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2})
-    return torch
+        _FLOATS = (torch.float32, torch.bfloat16)
+        _TABLES = (*_FLOATS, torch.float8_e4m3fn)
+        _INT8 = (torch.int8,)
+        _MODULE = torch
+    return _MODULE
 
 
-def _gpu(torch, t, what):
+def _device(torch, t, what):
+    """The device of a call's first tensor, which is the current one."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a GPU tensor (got {t.device}); there is no CPU path")
-    if t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{what} is on {t.device}, not on the current device")
-    return t
+    return dev
 
 
-def _rows(torch, t, what, dtypes):
-    """A 2-D tensor of one of `dtypes` with unit column stride."""
-    _gpu(torch, t, what)
+def _on(torch, t, what, dev):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _device(torch, t, what)  # says what is wrong
+        raise ValueError(f"{what} is on {t.device}, not on the current device")
+
+
+def _rows(torch, t, what, dtypes, dev):
+    """Rows, columns and row stride of a 2-D tensor of one of `dtypes` with
+    unit column stride.  A tensor of one row has whatever stride it was made
+    with, which no access uses."""
+    _on(torch, t, what, dev)
     if t.dtype not in dtypes:
         raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] != 1):
         raise ValueError(f"{what} must be 2-D with unit column stride")
-    return t
+    m, n = shape
+    return m, n, stride[0] if m > 1 else max(n, 1)
 
 
-def _vector(torch, t, what, n, dtype=None):
-    _gpu(torch, t, what)
-    if t.dtype != (dtype or torch.float32):
-        raise TypeError(f"{what} must be {dtype or torch.float32} (got {t.dtype})")
-    if not t.is_contiguous() or t.numel() != n:
+def _vector(torch, t, what, n, dev):
+    _on(torch, t, what, dev)
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{what} must be torch.float32 (got {t.dtype})")
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous with {n} elements")
-    return t
+    return t.data_ptr()
 
 
-def _ld(t):
-    """Row stride of a 2-D tensor; a tensor of one row has whatever stride it
-    was made with, which no access uses."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _new(torch, shape, like, stream, dtype):
+def _new(shape, like, stream, dtype):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     return _empty(shape, like.device, stream, dtype)
 
 
-def _tokens(torch, tokens):
-    _gpu(torch, tokens, "tokens")
-    if tokens.dtype != torch.int32:
+def _handle(torch, stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _tokens(torch, tokens, dev):
+    _on(torch, tokens, "tokens", dev)
+    if tokens.dtype is not torch.int32:
         raise TypeError(f"tokens must be torch.int32 (got {tokens.dtype})")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
-    return tokens
+    return tokens.numel()
 
 
-def _token_rows(torch, t, what, tokens, dim, dtypes):
-    """One row of `dim` for each token: (n, dim), or contiguous with the
-    tokens' shape and dim."""
+def _token_rows(torch, t, what, tokens, dim, dtypes, dev):
+    """Row stride of one row of `dim` for each token: (n, dim), or contiguous
+    with the tokens' shape and dim."""
     if t.dim() != 2:
         if t.shape != (*tokens.shape, dim) or not t.is_contiguous():
             raise ValueError(f"{what} must be (tokens, dim), or contiguous with the tokens' "
                              "shape and dim")
         t = t.view(-1, dim)
-    _rows(torch, t, what, dtypes)
-    if t.shape != (tokens.numel(), dim):
+    m, n, ld = _rows(torch, t, what, dtypes, dev)
+    if m != tokens.numel() or n != dim:
         raise ValueError(f"{what} must have a row of {dim} for each of {tokens.numel()} tokens")
-    return t
+    return ld
+
+
+def _out_dtype(out_dtype):
+    if out_dtype not in _FLOATS:
+        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16 (got {out_dtype})")
+    return out_dtype
 
 
 def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream=None):
@@ -91,24 +121,23 @@ def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream
     (`out_dtype`; the table's type if that is one of them, else float32)."""
     torch = _torch()
     lib = load()
-    _rows(torch, table, "table", (torch.float32, torch.bfloat16, torch.float8_e4m3fn))
-    _tokens(torch, tokens)
-    rows, dim = table.shape
+    dev = _device(torch, table, "table")
+    rows, dim, ld = _rows(torch, table, "table", _TABLES, dev)
+    n = _tokens(torch, tokens, dev)
     if out is None:
         if out_dtype is None:
-            out_dtype = torch.float32 if table.dtype == torch.float8_e4m3fn else table.dtype
-        if out_dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16 (got {out_dtype})")
-        out = _new(torch, (*tokens.shape, dim), table, stream, out_dtype)
+            out_dtype = table.dtype if table.dtype in _FLOATS else torch.float32
+        out = _new((*tokens.shape, dim), table, stream, _out_dtype(out_dtype))
         ld_out = dim
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out and out_dtype disagree")
-        ld_out = _ld(_token_rows(torch, out, "out", tokens, dim, (torch.float32, torch.bfloat16)))
-    _check(lib.emb_lookup_scaled(tokens.numel(), rows, dim, table.data_ptr(), _ld(table),
-                                 _CODES[table.dtype], tokens.data_ptr(), scale, out.data_ptr(),
-                                 ld_out, _CODES[out.dtype], _stream(stream)),
-           "emb_lookup_scaled")
+        ld_out = _token_rows(torch, out, "out", tokens, dim, _FLOATS, dev)
+    status = lib.emb_lookup_scaled(n, rows, dim, table.data_ptr(), ld, _CODES[table.dtype],
+                                   tokens.data_ptr(), scale, out.data_ptr(), ld_out,
+                                   _CODES[out.dtype], _handle(torch, stream, dev))
+    if status:
+        _check(status, "emb_lookup_scaled")
     return out
 
 
@@ -127,41 +156,43 @@ def emb_lookup_grad(grad, tokens, rows=None, scale=1.0, out_dtype=None, out=None
     without it one is allocated for the call."""
     torch = _torch()
     lib = load()
-    types = (torch.float32, torch.bfloat16)
-    _tokens(torch, tokens)
     if not isinstance(grad, torch.Tensor) or grad.dim() < 1:
         raise TypeError("grad must be a torch.Tensor with a row for each token")
-    grad2 = _token_rows(torch, grad, "grad", tokens, grad.shape[-1], types)
-    dim = grad2.shape[1]
+    dev = _device(torch, grad, "grad")
+    n = _tokens(torch, tokens, dev)
+    dim = grad.shape[-1]
+    ld = _token_rows(torch, grad, "grad", tokens, dim, _FLOATS, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         if rows is None:
             raise ValueError("rows is required without out")
-        if out_dtype is None:
-            out_dtype = grad2.dtype
-        if out_dtype not in types:
-            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16 (got {out_dtype})")
-        out = _new(torch, (rows, dim), grad2, stream, out_dtype)
+        out = _new((rows, dim), grad, stream,
+                   grad.dtype if out_dtype is None else _out_dtype(out_dtype))
+        ld_out = dim
     else:
-        _rows(torch, out, "out", types)
+        out_rows, out_dim, ld_out = _rows(torch, out, "out", _FLOATS, dev)
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out and out_dtype disagree")
-        if out.shape[1] != dim or (rows is not None and out.shape[0] != rows):
+        if out_dim != dim or (rows is not None and out_rows != rows):
             raise ValueError("out must be (rows, dim)")
-        rows = out.shape[0]
-    n = tokens.numel()
+        rows = out_rows
     if workspace is None:
-        workspace = _new(torch, (lib.emb_lookup_grad_workspace_bytes(n, rows, dim),), grad2,
-                         stream, torch.uint8)
+        size = lib.emb_lookup_grad_workspace_bytes(n, rows, dim)
+        if size:
+            workspace = _new((size,), grad, stream, torch.uint8)
     else:
-        _gpu(torch, workspace, "workspace")
+        _on(torch, workspace, "workspace", dev)
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous uint8 tensor")
-    _check(lib.emb_lookup_grad(n, rows, dim, grad2.data_ptr(), _ld(grad2), _CODES[grad2.dtype],
-                               tokens.data_ptr(), scale, 1 if accumulate else 0, out.data_ptr(),
-                               _ld(out), _CODES[out.dtype], workspace.data_ptr(),
-                               workspace.numel(), _stream(stream)), "emb_lookup_grad")
+        size = workspace.numel()
+    status = lib.emb_lookup_grad(n, rows, dim, grad.data_ptr(), ld, _CODES[grad.dtype],
+                                 tokens.data_ptr(), scale, 1 if accumulate else 0,
+                                 out.data_ptr(), ld_out, _CODES[out.dtype],
+                                 workspace.data_ptr() if workspace is not None else None, size,
+                                 _handle(torch, stream, dev))
+    if status:
+        _check(status, "emb_lookup_grad")
     return out
 
 
@@ -172,38 +203,43 @@ def rms_norm_residual_i8(x, weight=None, residual=None, eps=1e-6, out_h=None, ou
     `out_h` may be x or residual."""
     torch = _torch()
     lib = load()
-    types = (torch.float32, torch.bfloat16)
-    _rows(torch, x, "x", types)
-    m, dim = x.shape
-    wp = None if weight is None else _vector(torch, weight, "weight", dim).data_ptr()
+    dev = _device(torch, x, "x")
+    m, dim, ldx = _rows(torch, x, "x", _FLOATS, dev)
+    dtype = x.dtype
+    wp = None if weight is None else _vector(torch, weight, "weight", dim, dev)
     rp, ldr, hp, ldh = None, 0, None, 0
     if residual is None:
         if out_h is not None:
             raise ValueError("out_h needs a residual (without one, h is x)")
         h = x
     else:
-        _rows(torch, residual, "residual", (x.dtype,))
-        if residual.shape != x.shape:
+        rm, rdim, ldr = _rows(torch, residual, "residual", (dtype,), dev)
+        if rm != m or rdim != dim:
             raise ValueError("residual must have x's shape")
         if out_h is None:
-            h = _new(torch, (m, dim), x, stream, x.dtype)
+            h, ldh = _new((m, dim), x, stream, dtype), dim
         else:
-            h = _rows(torch, out_h, "out_h", (x.dtype,))
-            if h.shape != x.shape:
+            h = out_h
+            hm, hdim, ldh = _rows(torch, h, "out_h", (dtype,), dev)
+            if hm != m or hdim != dim:
                 raise ValueError("out_h must have x's shape")
-        rp, ldr, hp, ldh = residual.data_ptr(), _ld(residual), h.data_ptr(), _ld(h)
+        rp, hp = residual.data_ptr(), h.data_ptr()
     if out_codes is None:
-        out_codes = _new(torch, (m, dim), x, stream, torch.int8)
-    elif _rows(torch, out_codes, "out_codes", (torch.int8,)).shape != x.shape:
-        raise ValueError("out_codes must have x's shape")
-    if out_scale is None:
-        out_scale = _new(torch, (m,), x, stream, torch.float32)
+        out_codes, ldq = _new((m, dim), x, stream, torch.int8), dim
     else:
-        _vector(torch, out_scale, "out_scale", m)
-    _check(lib.rms_norm_residual_i8(m, dim, x.data_ptr(), _ld(x), rp, ldr, _CODES[x.dtype], wp,
-                                    eps, hp, ldh, out_codes.data_ptr(), _ld(out_codes),
-                                    out_scale.data_ptr(), _stream(stream)),
-           "rms_norm_residual_i8")
+        qm, qdim, ldq = _rows(torch, out_codes, "out_codes", _INT8, dev)
+        if qm != m or qdim != dim:
+            raise ValueError("out_codes must have x's shape")
+    if out_scale is None:
+        out_scale = _new((m,), x, stream, torch.float32)
+        sp = out_scale.data_ptr()
+    else:
+        sp = _vector(torch, out_scale, "out_scale", m, dev)
+    status = lib.rms_norm_residual_i8(m, dim, x.data_ptr(), ldx, rp, ldr, _CODES[dtype], wp, eps,
+                                      hp, ldh, out_codes.data_ptr(), ldq, sp,
+                                      _handle(torch, stream, dev))
+    if status:
+        _check(status, "rms_norm_residual_i8")
     return h, out_codes, out_scale
 
 
@@ -214,30 +250,28 @@ def linear_i8_bias_act(a, a_scale, w, w_scale, bias=None, act="none", out_dtype=
     given)."""
     torch = _torch()
     lib = load()
-    _rows(torch, a, "a", (torch.int8,))
-    _rows(torch, w, "w", (torch.int8,))
-    m, k = a.shape
-    n = w.shape[0]
-    if w.shape[1] != k:
+    dev = _device(torch, a, "a")
+    m, k, lda = _rows(torch, a, "a", _INT8, dev)
+    n, kw, ldw = _rows(torch, w, "w", _INT8, dev)
+    if kw != k:
         raise ValueError("w must be (N, K) with a's K")
-    _vector(torch, a_scale, "a_scale", m)
-    _vector(torch, w_scale, "w_scale", n)
-    bp = None if bias is None else _vector(torch, bias, "bias", n).data_ptr()
+    ap = _vector(torch, a_scale, "a_scale", m, dev)
+    wp = _vector(torch, w_scale, "w_scale", n, dev)
+    bp = None if bias is None else _vector(torch, bias, "bias", n, dev)
     if out is None:
-        if out_dtype is None:
-            out_dtype = torch.float32
-        if out_dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16 (got {out_dtype})")
-        out = _new(torch, (m, n), a, stream, out_dtype)
+        out = _new((m, n), a, stream,
+                   torch.float32 if out_dtype is None else _out_dtype(out_dtype))
+        ldc = n
     else:
-        _rows(torch, out, "out", (torch.float32, torch.bfloat16))
+        om, on, ldc = _rows(torch, out, "out", _FLOATS, dev)
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out and out_dtype disagree")
-        if out.shape != (m, n):
+        if om != m or on != n:
             raise ValueError("out must be (M, N)")
-    _check(lib.linear_i8_bias_act(m, n, k, a.data_ptr(), _ld(a), a_scale.data_ptr(), w.data_ptr(),
-                                  _ld(w), w_scale.data_ptr(), bp,
-                                  ACTS[act] if isinstance(act, str) else int(act), out.data_ptr(),
-                                  _ld(out), _CODES[out.dtype], _stream(stream)),
-           "linear_i8_bias_act")
+    status = lib.linear_i8_bias_act(m, n, k, a.data_ptr(), lda, ap, w.data_ptr(), ldw, wp, bp,
+                                    ACTS[act] if isinstance(act, str) else int(act),
+                                    out.data_ptr(), ldc, _CODES[out.dtype],
+                                    _handle(torch, stream, dev))
+    if status:
+        _check(status, "linear_i8_bias_act")
     return out

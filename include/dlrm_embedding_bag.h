@@ -604,9 +604,9 @@ DLRM_API int emb_lookup_scaled(int64_t num_tokens, int64_t rows, int32_t dim, co
  *               ld_out; must not overlap grad
  *   workspace   16-byte aligned, at least
  *               emb_lookup_grad_workspace_bytes(num_tokens, rows, dim) bytes
- *               (which returns 0 for sizes that the call refuses); its
- *               content needs no clearing and carries nothing to the next
- *               call
+ *               (which returns 0 for few tokens, where workspace may be NULL,
+ *               and for sizes that the call refuses); its content needs no
+ *               clearing and carries nothing to the next call
  */
 DLRM_API size_t emb_lookup_grad_workspace_bytes(int64_t num_tokens, int64_t rows, int32_t dim);
 DLRM_API int emb_lookup_grad(int64_t num_tokens, int64_t rows, int32_t dim, const void *grad,

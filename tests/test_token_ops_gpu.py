@@ -177,8 +177,30 @@ def test_grad(n, rows, dim, kind, grad, out):
     assert torch.equal(t.cpu()[torch.from_numpy(~named)], base[torch.from_numpy(~named)])
 
 
-def test_grad_more_tokens_than_one_round_of_tiles():
-    """Beyond 512 tiles of 4096 tokens a sorting workgroup takes several."""
+@pytest.mark.parametrize("kind", ["hot", "same", "uniform"])
+@pytest.mark.parametrize("n,rows,dim", [(63, 40, 100), (64, 5_000_000, 8), (65, 40, 72),
+                                        (1023, 300, 600), (1024, 50, 16), (1025, 7, 70),
+                                        (2049, 1_048_575, 3), (3000, 1_048_576, 3),
+                                        (4095, 900, 33), (4096, 10, 1040), (4097, 20, 1040),
+                                        (65536, 5000, 9), (65537, 5000, 9), (70000, 4_200_000, 2),
+                                        (9000, 4_200_000, 2)])
+def test_grad_at_the_sorts_borders(n, rows, dim, kind):
+    """Sizes around those where the sort's tile, key width or launches change."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(n)
+    tok = _draw_tokens(rng, n, rows, kind)
+    g = rng.standard_normal((n, dim)).astype(np.float32)
+    td, gd = torch.from_numpy(tok).cuda(), torch.from_numpy(g).cuda()
+    got = fw.emb_lookup_grad(gd, td, rows)
+    named = _check_grad(got, g.astype(np.float64), tok, rows, 1.0, "f32")
+    assert np.all(_np64(got)[~named] == 0.0)
+    assert torch.equal(got, fw.emb_lookup_grad(gd, td, rows))
+
+
+def test_grad_more_tokens_than_one_merge_takes():
+    """Beyond 64 tiles of 4096 tokens runs are merged twice."""
     import torch
 
     import dlrm_embedding_bag_amd as fw
@@ -572,12 +594,13 @@ def test_given_workspace_and_refusals():
 
     import dlrm_embedding_bag_amd as fw
     table, tok, res, wn, w8, sw, grad = _chain_state(300, 40, 24, 16, 4)
-    need = fw.emb_lookup_grad_workspace_bytes(300, 40, 24)
+    many, tok_many = grad.repeat(20, 1), tok.repeat(20)
+    need = fw.emb_lookup_grad_workspace_bytes(6000, 40, 24)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")   # content does not matter
-    got = fw.emb_lookup_grad(grad, tok, 40, workspace=ws)
-    assert torch.equal(got, fw.emb_lookup_grad(grad, tok, 40))
+    got = fw.emb_lookup_grad(many, tok_many, 40, workspace=ws)
+    assert torch.equal(got, fw.emb_lookup_grad(many, tok_many, 40))
     with pytest.raises(fw.DlrmError) as e:
-        fw.emb_lookup_grad(grad, tok, 40, workspace=ws[:-1])
+        fw.emb_lookup_grad(many, tok_many, 40, workspace=ws[:-1])
     assert e.value.name == "DLRM_ERR_WORKSPACE"
     with pytest.raises(ValueError):
         fw.emb_lookup_grad(grad, tok)                                  # no rows, no out

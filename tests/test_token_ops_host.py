@@ -63,11 +63,12 @@ def test_grad_refusals(lib):
     assert _grad(lib, grad=None) == NULL
     assert _grad(lib, tok=None) == NULL
     assert _grad(lib, out=None) == NULL
-    need = lib.emb_lookup_grad_workspace_bytes(4, 10, 8)
+    n = 100000
+    need = lib.emb_lookup_grad_workspace_bytes(n, 10, 8)
     assert need > 0
-    assert _grad(lib, ws=None) == WORKSPACE
-    assert _grad(lib, wsb=need - 1) == WORKSPACE
-    assert _grad(lib, ws=FAKE + 8) == WORKSPACE
+    assert _grad(lib, n=n, ws=None) == WORKSPACE
+    assert _grad(lib, n=n, wsb=need - 1) == WORKSPACE
+    assert _grad(lib, n=n, ws=FAKE + 8) == WORKSPACE
     # no tokens and nothing to write
     assert _grad(lib, n=0, acc=1, grad=None, tok=None, out=None, ws=None, wsb=0) == OK
 

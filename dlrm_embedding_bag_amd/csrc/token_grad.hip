@@ -49,6 +49,7 @@ constexpr int kSearches = 4;                  // binary searches of a thread in 
 constexpr int kFillBlocks = 2048;             // zero-filling workgroups per launch
 constexpr int kReduceThreads = 256;
 constexpr int kMaxPer = 8;                    // tokens that a lane group adds up alone
+constexpr int kMaxPart = 256 * kMaxPer;       // tokens of a part
 constexpr int kFixThreads = 256;
 constexpr int kUnroll = 8;                    // partial sums of a lane group in flight
 constexpr int64_t kMaxBlocks = 1 << 22;       // a launch holds fewer than 2^32 threads
@@ -308,8 +309,8 @@ __device__ __forceinline__ Lanes lanes_of(int log2g, int64_t slice, int dim) {
 //   key(i), pos(i)   row and position of sorted token i
 //   open             the row of t0 began before it: group 0 takes it up from
 //                    what begin(acc) gives
-//   goes_on          the row of t1 - 1 goes on after it: end(acc, began) takes
-//                    its sum so far (began: in this call)
+//   goes_on          the row of t1 - 1 goes on after it: end(row, acc) takes its
+//                    sum so far
 //   done(row, acc)   takes a finished row
 template <typename TG, int PER, typename Key, typename Pos, typename Begin, typename End,
           typename Done>
@@ -384,7 +385,7 @@ __device__ __forceinline__ void reduce_tokens(const GradParams &g, const Lanes &
   }
   __syncthreads();
   // adds the heads of the waves after this one that the row reaches
-  auto walk = [&](uint32_t row, bool began) {
+  auto walk = [&](uint32_t row) {
     const int stride = (kWave >> l.log2g) * PER;
     int w = wave + 1;
     for (int s = t0 + w * stride; s < t1 && key(s) == row; s += stride, ++w) {
@@ -396,16 +397,16 @@ __device__ __forceinline__ void reduce_tokens(const GradParams &g, const Lanes &
       }
     }
     if (goes_on && key(t1 - 1) == row)
-      end(acc, began);
+      end(row, acc);
     else
       done(row, acc);
   };
-  if (tail) walk(key(b - 1), true);
+  if (tail) walk(key(b - 1));
   if (open && l.group == 0 && l.live && t0 < t1) {
     begin(acc);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] += head[e];
-    walk(key(t0), false);
+    walk(key(t0));
   }
 }
 
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(SmallParams p) {
               acc[4 + e] = carry[round][1][lane][e];
             }
           },
-          [&](const float (&acc)[8], bool) {
+          [&](uint32_t, const float (&acc)[8]) {
             carry[round ^ 1][0][lane] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
             carry[round ^ 1][1][lane] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
           },
@@ -637,20 +638,22 @@ struct ReduceParams {
   const int32_t *key, *pos;  // sorted
   float *head, *tail;        // partial sums, one row of dim each per part
   int64_t parts;
-  int part;                  // tokens per part: lane groups * per
+  int part;                  // tokens per part: rounds of lane groups * per
   int log2g;                 // lanes per group
   int slices;                // column slices of 8 << log2g
 };
 
 template <typename TG, typename TO, int PER>
 __global__ __launch_bounds__(kReduceThreads) void reduce_kernel(ReduceParams p) {
-  __shared__ uint32_t keys[kReduceThreads * PER + 2];  // from the token before the part on
-  __shared__ uint32_t where[kReduceThreads * PER];
+  __shared__ uint32_t keys[kMaxPart + 2];  // from the token before the part on
+  __shared__ uint32_t where[kMaxPart];
   __shared__ f32x4_t heads[2 * kReduceThreads];
+  __shared__ f32x4_t carry[2][2][kWave];   // the open row's sum, by round parity
   const GradParams &g = p.g;
   for (int64_t item = blockIdx.x; item < p.parts * p.slices; item += gridDim.x) {
     const int64_t part = item / p.slices, s0 = part * p.part;
     const Lanes l = lanes_of(p.log2g, item - part * p.slices, g.dim);
+    const int lane = threadIdx.x & ((1 << p.log2g) - 1);
     int nv = 0;  // tokens of the part that are in the table
     for (int i = threadIdx.x; i < p.part + 2; i += kReduceThreads) {
       const int64_t s = s0 + i - 1;
@@ -660,26 +663,39 @@ __global__ __launch_bounds__(kReduceThreads) void reduce_kernel(ReduceParams p) 
     __syncthreads();
     for (int i = threadIdx.x; i - (int)threadIdx.x < p.part; i += kReduceThreads)
       nv += __syncthreads_count(i < p.part && keys[1 + (i < p.part ? i : 0)] < (uint32_t)g.rows);
-    if (nv > 0) {
-      const bool open = s0 > 0 && keys[0] == keys[1];
-      const bool goes_on = nv == p.part && keys[nv + 1] == keys[nv];
+    auto key = [&](int i) { return keys[1 + i]; };
+    // a row that began in an earlier part (no token has the row number rows)
+    const uint32_t earlier = nv > 0 && s0 > 0 && keys[0] == keys[1] ? keys[0] : (uint32_t)g.rows;
+    const bool leaves = nv == p.part && keys[nv + 1] == keys[nv];
+    int round = 0;
+    for (int t0 = 0; t0 < nv; t0 += l.groups * PER, round ^= 1) {
+      const int t1 = t0 + l.groups * PER < nv ? t0 + l.groups * PER : nv;
+      const bool last = t1 == nv;
       reduce_tokens<TG, PER>(
-          g, l, 0, nv, open, goes_on, heads, [&](int i) { return keys[1 + i]; },
-          [&](int i) { return where[i]; },
+          g, l, t0, t1, t0 > 0 ? key(t0 - 1) == key(t0) : earlier == key(0),
+          last ? leaves : key(t1 - 1) == key(t1), heads, key, [&](int i) { return where[i]; },
           [&](float (&acc)[8]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-          },
-          [&](const float (&acc)[8], bool began) {
-            store_chunk<F32>((began ? p.tail : p.head) + part * g.dim, l.c, g.dim, acc);
+            for (int e = 0; e < 4; ++e) {
+              acc[e] = t0 > 0 ? carry[round][0][lane][e] : 0.0f;
+              acc[4 + e] = t0 > 0 ? carry[round][1][lane][e] : 0.0f;
+            }
           },
           [&](uint32_t row, const float (&acc)[8]) {
-            // a row that began in an earlier part ends here
-            if (open && row == keys[0])
+            if (last) {
+              store_chunk<F32>((row == earlier ? p.head : p.tail) + part * g.dim, l.c, g.dim, acc);
+            } else {
+              carry[round ^ 1][0][lane] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+              carry[round ^ 1][1][lane] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
+            }
+          },
+          [&](uint32_t row, const float (&acc)[8]) {
+            if (row == earlier)
               store_chunk<F32>(p.head + part * g.dim, l.c, g.dim, acc);
             else
               finish_row<TO>(g, row, l.c, acc);
           });
+      __syncthreads();  // heads are read before the next round writes them
     }
     __syncthreads();  // before the next item's keys
   }
@@ -783,7 +799,9 @@ Layout plan_layout(int64_t n, int64_t rows, int dim) {
   const int groups = kReduceThreads >> l.log2g;
   l.per = kMaxPer;
   while (l.per > 2 && n / ((int64_t)groups * l.per) * l.slices < 1024) l.per /= 2;
+  // long parts leave fewer partial sums: as long as 1024 workgroups remain
   l.part = groups * l.per;
+  while (l.part * 2 <= kMaxPart && n / (l.part * 2) * l.slices >= 1024) l.part *= 2;
   l.parts = (n + l.part - 1) / l.part;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {

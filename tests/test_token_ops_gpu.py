@@ -476,6 +476,21 @@ def test_product_large(m, n, k):
     _check_product(got, a, sa, w, sw, b, "relu", "f32")
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [
+    (65, 64, 16), (100, 70, 80), (129, 1000, 48), (500, 601, 1008), (70, 4100, 1168),   # 64 x 64
+    (2000, 2100, 32), (2000, 2103, 272), (1920, 2177, 576),                             # 128 x 128
+    (3000, 3100, 48), (3000, 3101, 464), (2900, 3333, 320), (3073, 2817, 64 * 9)])      # 256 x 256
+def test_product_of_rows_on_16_bytes(m, n, k, out):
+    """Tiles of each size whose k ends before the first stage, inside one, and
+    after few or many of them, and whose rows and columns end inside a tile."""
+    import dlrm_embedding_bag_amd as fw
+    a, sa, w, sw, b = _product_case(m, n, k, m + n + k)
+    got = fw.linear_i8_bias_act(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), b.cuda(), "none",
+                                out_dtype=_dt(out))
+    _check_product(got, a, sa, w, sw, b, "none", out)
+
+
 @pytest.mark.parametrize("m", [1, 40, 200])
 def test_product_longest_sum(m):
     """k at its limit with every product at its largest: 2^14 * 131071 < 2^31."""

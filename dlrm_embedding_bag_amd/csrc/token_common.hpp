@@ -150,6 +150,48 @@ __device__ __forceinline__ void store_chunk(typename T::S *row, int c, int dim,
   }
 }
 
+// The value of lane (lane ^ X), by register moves; every lane is active.
+template <int X>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+  const int i = (int)v;
+  if constexpr (X == 1) {          // quad_perm [1,0,3,2]
+    return __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, true);
+  } else if constexpr (X == 2) {   // quad_perm [2,3,0,1]
+    return __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, true);
+  } else if constexpr (X == 3) {   // quad_perm [3,2,1,0]
+    return __builtin_amdgcn_update_dpp(0, i, 0x1B, 0xF, 0xF, true);
+  } else if constexpr (X == 4) {
+    return lane_xor<3>(lane_xor<7>(v));
+  } else if constexpr (X == 7) {   // mirror of 8 lanes
+    return __builtin_amdgcn_update_dpp(0, i, 0x141, 0xF, 0xF, true);
+  } else if constexpr (X == 8) {   // rotation of 16 lanes by 8
+    return __builtin_amdgcn_update_dpp(0, i, 0x128, 0xF, 0xF, true);
+  } else if constexpr (X == 15) {  // mirror of 16 lanes
+    return __builtin_amdgcn_update_dpp(0, i, 0x140, 0xF, 0xF, true);
+  } else if constexpr (X == 16) {
+    // the swap leaves the lower rows' values in one result, the upper in the other
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return threadIdx.x & 16 ? r[0] : r[1];
+  } else if constexpr (X == 31) {
+    return lane_xor<16>(lane_xor<15>(v));
+  } else if constexpr (X == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return threadIdx.x & 32 ? r[0] : r[1];
+  } else {
+    static_assert(X == 63);
+    return lane_xor<32>(lane_xor<31>(v));
+  }
+}
+template <int X>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+  return (uint64_t)lane_xor<X>((uint32_t)(v >> 32)) << 32 | lane_xor<X>((uint32_t)v);
+}
+
+template <int X>
+__device__ __forceinline__ double lane_xor(double v) {
+  return __builtin_bit_cast(double, lane_xor<X>(__builtin_bit_cast(uint64_t, v)));
+}
+
 // Eight elements as they were read, for loads that wait in registers: half the
 // registers of float32 for bfloat16 rows.
 template <typename T>

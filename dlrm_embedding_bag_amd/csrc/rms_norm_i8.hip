@@ -218,7 +218,8 @@ __global__ __launch_bounds__(TPR *rows_of_block<TPR>()) void norm_kernel(NormPar
       if (c < p.dim) {
         load_w(p.weight, c, p.dim, w[i]);
         if (RES && there)
-          store_chunk<T, true>((typename T::S *)p.h + m * p.ldh, c, p.dim, h[i]);
+          store_chunk<T, sizeof(typename T::S) == 2>((typename T::S *)p.h + m * p.ldh, c, p.dim,
+                                                     h[i]);
         accumulate(h[i], w[i], ss, mx, bad);
       }
     }

@@ -12,6 +12,7 @@
 
 namespace dlrm {
 
+typedef uint32_t u32_u __attribute__((aligned(1)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
@@ -74,6 +75,35 @@ __device__ __forceinline__ void load8<FP8>(const uint8_t *p, float (&v)[8]) {
   }
 }
 
+// Four likewise.
+template <typename T>
+__device__ __forceinline__ void load4(const typename T::S *p, float (&v)[4]);
+template <>
+__device__ __forceinline__ void load4<F32>(const float *p, float (&v)[4]) {
+  const f32x4_u a = *reinterpret_cast<const f32x4_u *>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = a[e];
+}
+template <>
+__device__ __forceinline__ void load4<BF16>(const uint16_t *p, float (&v)[4]) {
+  const u32x2_u a = *reinterpret_cast<const u32x2_u *>(p);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    v[2 * e] = bf16_lo(a[e]);
+    v[2 * e + 1] = bf16_hi(a[e]);
+  }
+}
+template <>
+__device__ __forceinline__ void load4<FP8>(const uint8_t *p, float (&v)[4]) {
+  const uint32_t a = *reinterpret_cast<const u32_u *>(p);
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)a, false);
+  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)a, true);
+  v[0] = lo[0];
+  v[1] = lo[1];
+  v[2] = hi[0];
+  v[3] = hi[1];
+}
+
 template <typename T>
 __device__ __forceinline__ float load1(const typename T::S *p);
 template <>
@@ -126,26 +156,38 @@ __device__ __forceinline__ void store1(typename T::S *p, float v) {
     *p = to_bf16(v);
 }
 
-// Elements [c, c + 8) of a row of `dim` elements; those past the row read as
-// zero and are not stored.
-template <typename T>
+// Elements [c, c + N) of a row of `dim` elements (N 4 or 8); those past the row
+// read as zero and are not stored.
+template <typename T, int N>
 __device__ __forceinline__ void load_chunk(const typename T::S *row, int c, int dim,
-                                           float (&v)[8]) {
-  if (c + 8 <= dim) {
-    load8<T>(row + c, v);
+                                           float (&v)[N]) {
+  static_assert(N == 4 || N == 8);
+  if (c + N <= dim) {
+    if constexpr (N == 8)
+      load8<T>(row + c, v);
+    else
+      load4<T>(row + c, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < dim ? load1<T>(row + c + e) : 0.0f;
+    for (int e = 0; e < N; ++e) v[e] = c + e < dim ? load1<T>(row + c + e) : 0.0f;
   }
 }
-template <typename T, bool NT = false>
+template <typename T, bool NT = false, int N>
 __device__ __forceinline__ void store_chunk(typename T::S *row, int c, int dim,
-                                            const float (&v)[8]) {
-  if (c + 8 <= dim) {
-    store8<T, NT>(row + c, v);
+                                            const float (&v)[N]) {
+  static_assert(N == 8 || (N == 4 && sizeof(typename T::S) == 4));
+  if (c + N <= dim) {
+    if constexpr (N == 8) {
+      store8<T, NT>(row + c, v);
+    } else {
+      u32x4_t a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(v[e]);
+      put16<NT>(row + c, a);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < N; ++e)
       if (c + e < dim) store1<T>(row + c + e, v[e]);
   }
 }

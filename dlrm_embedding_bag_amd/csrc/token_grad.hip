@@ -46,7 +46,7 @@ constexpr int kMaxFan = 16;                   // and else
 constexpr int kMergeWaves = 8;
 constexpr int kMergeThreads = kMergeWaves * kWave;
 constexpr int kSearches = 4;                  // binary searches of a thread in flight
-constexpr int kFillBlocks = 2048;             // zero-filling workgroups per launch
+constexpr int kFillBlocks = 1 << 16;          // zero-filling workgroups per launch, at most
 constexpr int kReduceThreads = 256;
 constexpr int kMaxPer = 8;                    // tokens that a lane group adds up alone
 constexpr int kMaxPart = 256 * kMaxPer;       // tokens of a part

@@ -10,6 +10,18 @@
 // W is fed as the first operand, so a lane's 4 accumulators are 4 consecutive
 // columns of one row of C.  Rows may start at any byte (a K of odd length):
 // global memory takes 16-byte loads at any address.
+//
+// Three kernels, by the number of rows and the rows' alignment (launch_typed):
+//   few_rows   up to 64 rows: bound by reading W.  1 x 8192 x 8192: 13.4 us,
+//              5.0 TB/s; 32 x 8192 x 8192: 18.5 us, the rest A's 64 MB of L2
+//              reads (every CU reads all of A)
+//   staged     rows on 16 bytes.  8192^3: 440-500 us, 2.2-2.5 POP/s, where
+//              power holds the matrix cores at 1.8 GHz (all-zero operands take
+//              330 us) and they are busy 57% of the cycles; 128 x 8192 x 8192:
+//              16 us, W's bytes
+//   gemm       any rows, through registers.  2048 x 512 x 415: 6.7 us, one
+//              memory latency for each of four slabs of k; 4001 x 4099 x 4093:
+//              185 us
 #include <math.h>
 
 #include <type_traits>
@@ -560,6 +572,10 @@ void launch_few(const LinearI8Params &p, hipStream_t stream) {
                 dim3(kFewWaves * kWave), 0, stream, p);
 }
 
+// Tiles of 256 where they make more than half as many workgroups as CUs
+// (3000 x 3000 x 3008: 44 us, 52 with 128, 55 with 64; 1024 x 8192 x 8192, 128
+// of them: 93, 87, 96); of 128 where they make 256 (1000 x 4096 x 4096: 27 us,
+// 30 with 64; 256 x 4096 x 4096, 64 of them: 21 and 10); else of 64.
 template <typename TO>
 hipError_t launch_typed(const LinearI8Params &p, hipStream_t stream) {
   const bool many = p.N >= 8192;  // columns: two 16-column fragments still make 256 workgroups

@@ -16,17 +16,25 @@
 // up its share of the sorted order; others write zeros to the rows that no
 // token names.
 //
-// Beyond, four launches (five or six for millions of tokens):
+// Beyond, four launches (more where one merge does not reach all tokens):
 //   tile_sort   tiles of kTile tokens, each sorted by one workgroup
-//   merge       a token's place among up to kMaxFan sorted runs is its place
-//               in its own run plus, for each other run, a binary search:
-//               thousands of independent searches that stay in the caches,
-//               in one launch where a radix sort takes two for each digit
+//   merge       a token's place among the sorted runs is its place in its own
+//               run plus, for each other run, a binary search: thousands of
+//               independent searches that stay in the caches, in one launch
+//               where a radix sort takes two for each digit
 //   reduce      workgroups add up equal parts of the sorted order; a row that
 //               crosses a border leaves partial sums
 //   fix         adds those in order
 // Without accumulate every row of out is written: the sort's launches occupy
 // few CUs, so their grids carry further workgroups that fill out with zeros.
+//
+// Kernel times of Zipf batches (us):    sort  merge  reduce  fix
+//   40960 x 64 f32 into 1M rows            7     11      8     5   launches and
+//     the searches' chain bound it; its 18 MB would take 4
+//   65536 x 1024 bf16, 100000 rows f32    33     42     44     6   400 MB of
+//     zeros behind the sort (6 TB/s), then 134 MB of gradients and 80 MB of
+//     rows (4.9 TB/s): memory bounds it, but for the merge's 13 us
+//   160 x 16 (one launch): 5; 1000 x 64: 11
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -40,7 +48,8 @@ constexpr int kThreads = 512;                 // of a sorting workgroup
 constexpr int kWaves = kThreads / kWave;
 constexpr int kFew = 2;                       // tokens of a thread that sorts few,
 constexpr int kMany = 4;                      // and many
-constexpr int kTile = kMany * kThreads;       // tokens that one workgroup sorts
+constexpr int kTile = kMany * kThreads;       // tokens that one workgroup sorts (2048 take 7 us,
+                                              // 4096 in twice the threads 14)
 constexpr int kOneMerge = 32;                 // runs merged at once where that ends it,
 constexpr int kMaxFan = 16;                   // and else
 constexpr int kMergeWaves = 8;

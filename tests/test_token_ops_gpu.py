@@ -541,6 +541,52 @@ def test_product_rows_without_a_scale(m, n, k):
         _check_product(got[keep], a[keep], sa[keep], w, sw, b, act, "f32")
 
 
+# ------------------------------------------------- offsets beyond 32 bits --
+def test_lookup_and_gradient_far_into_a_table():
+    """A table of 2.2 billion elements: its last rows lie beyond 2^31 elements
+    and 2^32 bytes."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rows, dim = 1_100_000, 2048
+    table = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    tok = torch.tensor([rows - 1, 0, -1, rows - 2, 1_048_577, rows], dtype=torch.int32,
+                       device="cuda")
+    there = [0, 1, 3, 4]
+    values = torch.randn(len(there), dim, device="cuda").bfloat16()
+    table[tok[there].long()] = values
+    got = fw.emb_lookup_scaled(table, tok, 2.0)
+    assert torch.equal(got[there], values * 2.0)
+    assert torch.all(got[[2, 5]] == 0)
+    grad = torch.randn(6, dim, device="cuda").bfloat16()
+    fw.emb_lookup_grad(grad, tok, scale=1.0, out=table, accumulate=True)
+    assert torch.equal(table[tok[there].long()],
+                       (values.float() + grad[there].float()).bfloat16())
+    assert torch.all(table[rows - 3] == 0) and torch.all(table[1] == 0)
+    many = tok[:1].repeat(5000)      # the launches for many tokens
+    one = torch.full((1, dim), 0.5, device="cuda").expand(5000, dim)
+    out = table.zero_()
+    fw.emb_lookup_grad(one, many, scale=2.0 ** -10, out=out)
+    assert torch.all(out[rows - 1] == torch.tensor(5000 * 0.5 / 1024.0).bfloat16().cuda())
+    assert torch.all(out[rows - 2] == 0)
+
+
+@pytest.mark.parametrize("m", [1, 100])
+def test_product_far_into_the_weight(m):
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    n, k = 70_016, 32_768            # 2.3 billion bytes
+    g = torch.Generator(device="cuda").manual_seed(m)
+    w = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    a = torch.randint(-128, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
+    sa = torch.rand(m, generator=g, device="cuda") * 0.01
+    sw = torch.rand(n, generator=g, device="cuda") * 1e-4
+    got = fw.linear_i8_bias_act(a, sa, w, sw)
+    cols = torch.tensor([0, 1, 65_535, 65_536, n - 2, n - 1], device="cuda")
+    _check_product(got[:, cols], a, sa, w[cols], sw[cols], None, "none", "f32")
+
+
 # ------------------------------------------------------- streams and graphs --
 def _chain(fw, table, tok, res, wn, w8, sw, grad, rows):
     x = fw.emb_lookup_scaled(table, tok, 3.0)

@@ -19,9 +19,9 @@
 //              power holds the matrix cores at 1.8 GHz (all-zero operands take
 //              330 us) and they are busy 57% of the cycles; 128 x 8192 x 8192:
 //              16 us, W's bytes
-//   gemm       any rows, through registers.  2048 x 512 x 415: 6.7 us, one
-//              memory latency for each of four slabs of k; 4001 x 4099 x 4093:
-//              185 us
+//   gemm       any rows, through registers.  2048 x 512 x 415: 6.7-7.2 us;
+//              4001 x 4099 x 4093: 181 us, bound by loads that cross 16 bytes
+//              (4096^3 from rows on 16 bytes: 63)
 #include <math.h>
 
 #include <type_traits>
@@ -159,10 +159,13 @@ __device__ __forceinline__ void tile_of(int b, int tm, int tn, int &im, int &in)
 }
 
 // BM x BN tile on GM x GN waves; slabs of 128 bytes of k go through registers
-// to two LDS buffers (any alignment).  A row's 16-byte chunk c lies at place
-// c ^ (row % 8) of its 128-byte row: the rows that a ds_read_b128 touches
-// start on different banks.
-template <int BM, int BN, int GM, int GN, typename TO>
+// to two LDS buffers (any alignment), D slabs ahead: few workgroups wait for
+// memory at every slab (2000 x 100 x 5001: 32 us with one ahead, 24 with two, 21
+// with three; 1000 x 1000 x 1001: 9.1, 8.7, 9.0), larger tiles want the
+// registers (4000 x 2000 x 999: 24, 26, 36).  A row's 16-byte chunk c
+// lies at place c ^ (row % 8) of its 128-byte row: the rows that a ds_read_b128
+// touches start on different banks.
+template <int BM, int BN, int GM, int GN, int D, typename TO>
 __global__ __launch_bounds__(GM *GN *kWave) void gemm_kernel(LinearI8Params p, int tm, int tn) {
   constexpr int T = GM * GN * kWave;
   constexpr int FM = BM / GM / 16, FN = BN / GN / 16;
@@ -175,24 +178,25 @@ __global__ __launch_bounds__(GM *GN *kWave) void gemm_kernel(LinearI8Params p, i
   const int m0 = im * BM, n0 = in * BN;
   const int crow = tid / kChunks, cch = tid % kChunks;
 
-  i32x4_t ra[CA], rb[CB];
-  auto load = [&](int k0) {
-    const bool whole = k0 + kBK <= p.K;
-    const int k = k0 + cch * 16;
+  i32x4_t ra[D][CA], rb[D][CB];
+  const int whole = p.K / kBK, slabs = (p.K + kBK - 1) / kBK;
+  auto load = [&](int slab, i32x4_t (&ra)[CA], i32x4_t (&rb)[CB], auto inner) {
+    const int k = slab * kBK + cch * 16;
+    const bool full = inner || slab < whole;
 #pragma unroll
     for (int i = 0; i < CA; ++i) {
       const int m = m0 + crow + i * (T / kChunks);
       const int8_t *row = p.A + (int64_t)(m < p.M ? m : p.M - 1) * p.lda;
-      ra[i] = whole ? load16(row + k) : first_from(load16_tail(row, k, p.K), k, p.K);
+      ra[i] = full ? load16(row + k) : first_from(load16_tail(row, k, p.K), k, p.K);
     }
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
       const int n = n0 + crow + i * (T / kChunks);
       const int8_t *row = p.W + (int64_t)(n < p.N ? n : p.N - 1) * p.ldw;
-      rb[i] = whole ? load16(row + k) : load16_tail(row, k, p.K);
+      rb[i] = full ? load16(row + k) : load16_tail(row, k, p.K);
     }
   };
-  auto stage = [&](int buf) {
+  auto stage = [&](int buf, const i32x4_t (&ra)[CA], const i32x4_t (&rb)[CB]) {
 #pragma unroll
     for (int i = 0; i < CA; ++i) {
       const int r = crow + i * (T / kChunks);
@@ -211,13 +215,17 @@ __global__ __launch_bounds__(GM *GN *kWave) void gemm_kernel(LinearI8Params p, i
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
 
-  const int slabs = (p.K + kBK - 1) / kBK;
   const int fr = lane % 16, fc = lane / 16;
-  load(0);
-  stage(0);
-  for (int s = 0; s < slabs; ++s) {
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < slabs) load(d, ra[d], rb[d], std::false_type());
+  stage(0, ra[0], rb[0]);
+  // Slab s, in LDS; register slot u held it and takes slab s + D.  `inner`: that
+  // one is whole.
+  auto step = [&](int s, auto slot, auto inner) {
+    constexpr int U = decltype(slot)::value, NEXT = (U + 1) % D;
     __syncthreads();
-    if (s + 1 < slabs) load((s + 1) * kBK);
+    if (inner || s + D < slabs) load(s + D, ra[U], rb[U], inner);
     const i32x4_t *a = lds[s & 1] + (wm * (BM / GM)) * kChunks;
     const i32x4_t *b = lds[s & 1] + (BM + wn * (BN / GN)) * kChunks;
 #pragma unroll
@@ -233,8 +241,19 @@ __global__ __launch_bounds__(GM *GN *kWave) void gemm_kernel(LinearI8Params p, i
         for (int j = 0; j < FN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
-    if (s + 1 < slabs) stage((s + 1) & 1);
-  }
+    if (inner || s + 1 < slabs) stage((s + 1) & 1, ra[NEXT], rb[NEXT]);
+  };
+  auto steps = [&](int s, auto inner) {
+    step(s, std::integral_constant<int, 0>(), inner);
+    if constexpr (D > 1)
+      if (inner || s + 1 < slabs) step(s + 1, std::integral_constant<int, 1>(), inner);
+    if constexpr (D > 2)
+      if (inner || s + 2 < slabs) step(s + 2, std::integral_constant<int, 2>(), inner);
+  };
+  static_assert(D >= 1 && D <= 3);
+  int s = 0;
+  for (; s + 2 * D <= whole; s += D) steps(s, std::true_type());
+  for (; s < slabs; s += D) steps(s, std::false_type());
   store_tile<TO>(p, m0 + wm * (BM / GM), n0 + wn * (BN / GN), acc);
 }
 
@@ -547,10 +566,10 @@ __global__ __launch_bounds__(kFewWaves *kWave) void few_rows_kernel(LinearI8Para
   }
 }
 
-template <int BM, int BN, int GM, int GN, typename TO>
+template <int BM, int BN, int GM, int GN, int D, typename TO>
 void launch_tiles(const LinearI8Params &p, hipStream_t stream) {
   const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
-  launch_kernel(gemm_kernel<BM, BN, GM, GN, TO>, dim3((unsigned)(tm * tn)),
+  launch_kernel(gemm_kernel<BM, BN, GM, GN, D, TO>, dim3((unsigned)(tm * tn)),
                 dim3(GM * GN * kWave), 0, stream, p, tm, tn);
 }
 
@@ -592,13 +611,16 @@ hipError_t launch_typed(const LinearI8Params &p, hipStream_t stream) {
   const bool staged = staged_rows(p.A, p.lda) && staged_rows(p.W, p.ldw);
   if (tiles(256) > 128)
     staged ? launch_staged<256, 256, 2, 4, 64, TO>(p, stream)
-           : launch_tiles<256, 256, 2, 4, TO>(p, stream);
+           : launch_tiles<256, 256, 2, 4, 1, TO>(p, stream);
   else if (tiles(128) >= 256)
     staged ? launch_staged<128, 128, 2, 2, 64, TO>(p, stream)
-           : launch_tiles<128, 128, 2, 2, TO>(p, stream);
+           : launch_tiles<128, 128, 2, 2, 1, TO>(p, stream);
+  else if (staged)
+    launch_staged<64, 64, 2, 2, 128, TO>(p, stream);
+  else if (p.K > 2048)
+    launch_tiles<64, 64, 2, 2, 3, TO>(p, stream);
   else
-    staged ? launch_staged<64, 64, 2, 2, 128, TO>(p, stream)
-           : launch_tiles<64, 64, 2, 2, TO>(p, stream);
+    launch_tiles<64, 64, 2, 2, 2, TO>(p, stream);
   return hipGetLastError();
 }
 

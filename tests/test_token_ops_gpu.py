@@ -95,6 +95,24 @@ def test_lookup(n, rows, dim, kind, table, out):
     assert np.all(_np64(got)[~there] == 0.0)
 
 
+@pytest.mark.parametrize("table,out", [("f32", "f32"), ("bf16", "bf16"), ("fp8", "bf16"),
+                                       ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("n,dim", [(70001, 130), (20003, 1000), (150001, 72), (300007, 5)])
+def test_lookup_of_many_tokens(n, dim, table, out):
+    """Sizes at which a lane group takes one, two or four rows at once."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(n)
+    rows = 500
+    tok = torch.from_numpy(_draw_tokens(rng, n, rows, "hot"))
+    tab = torch.from_numpy(rng.standard_normal((rows, dim)).astype(np.float32)).to(_dt(table))
+    got = fw.emb_lookup_scaled(tab.cuda(), tok.cuda(), 0.5, out_dtype=_dt(out)).cpu()
+    # halves of the table's values are exact; one rounding to the output's type
+    want = torch.where((tok >= 0)[:, None], tab.float()[tok.clamp(0).long()] * 0.5, torch.zeros(()))
+    assert torch.equal(got, want.to(_dt(out)))
+
+
 @pytest.mark.parametrize("dim", [3, 64, 129])
 def test_lookup_strides_shapes_and_infinite_rows(dim):
     import torch
@@ -406,6 +424,46 @@ def test_norm_strides_and_in_place(dim, dtype):
     assert e[0].shape == (0, dim) and e[2].shape == (0,)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,dim", [(513, 700), (1000, 1024), (700, 1025), (600, 2048), (515, 4095),
+                                   (514, 8192), (1001, 31), (1003, 33), (1005, 65), (1007, 200),
+                                   (1009, 257)])
+def test_norm_of_many_rows(m, dim, dtype):
+    """Sizes at which rows share a wave, have one, or have a workgroup."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(m + dim)
+    x = torch.from_numpy(rng.standard_normal((m, dim)).astype(np.float32)).to(_dt(dtype))
+    r = torch.from_numpy(rng.standard_normal((m, dim)).astype(np.float32)).to(_dt(dtype))
+    w = torch.from_numpy((1 + 0.1 * rng.standard_normal(dim)).astype(np.float32))
+    x[3] = 0.0
+    r[3] = 0.0
+    h, q, s = fw.rms_norm_residual_i8(x.cuda(), w.cuda(), r.cuda(), eps=1e-6)
+    _check_norm(h, q, s, x, r, w, 1e-6)
+    # h in the residual's place
+    rd = r.cuda()
+    h, q2, s2 = fw.rms_norm_residual_i8(x.cuda(), w.cuda(), rd, eps=1e-6, out_h=rd)
+    assert h is rd and torch.equal(q, q2) and torch.equal(s, s2)
+    _check_norm(h, q2, s2, x, r, w, 1e-6)
+
+
+def test_norm_products_outside_float32():
+    """Products h * weight that overflow or vanish in float32 keep their codes."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(8)
+    x = torch.from_numpy(rng.standard_normal((6, 300)).astype(np.float32))
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    x[2, ::2] *= 1e25
+    for size in (1e30, 1e-30, 1.0):
+        w = torch.from_numpy((rng.standard_normal(300) * size).astype(np.float32))
+        h, q, s = fw.rms_norm_residual_i8(x.cuda(), w.cuda(), eps=1e-6)
+        _check_norm(h, q, s, x, None, w, 1e-6)
+
+
 def test_norm_many_short_rows():
     import torch
 
@@ -489,6 +547,20 @@ def test_product_of_rows_on_16_bytes(m, n, k, out):
     got = fw.linear_i8_bias_act(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), b.cuda(), "none",
                                 out_dtype=_dt(out))
     _check_product(got, a, sa, w, sw, b, "none", out)
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (1, 8200, 127), (16, 9000, 130), (32, 8200, 300), (50, 8195, 515), (64, 8192, 2176),  # few rows
+    (65, 70, 2601), (130, 90, 4099), (100, 129, 2050), (66, 65, 2047),                    # 64 x 64
+    (2000, 2100, 273), (1920, 2177, 45),                                                  # 128 x 128
+    (3000, 3100, 47), (2900, 3333, 321)])                                                 # 256 x 256
+def test_product_of_many_columns_and_of_rows_at_any_byte(m, n, k):
+    import dlrm_embedding_bag_amd as fw
+    a, sa, w, sw, b = _product_case(m, n, k, m + n + k)
+    for out in ("f32", "bf16"):
+        got = fw.linear_i8_bias_act(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), b.cuda(), "relu",
+                                    out_dtype=_dt(out))
+        _check_product(got, a, sa, w, sw, b, "relu", out)
 
 
 @pytest.mark.parametrize("m", [1, 40, 200])

@@ -55,6 +55,7 @@ constexpr int kMaxFan = 16;                   // and else
 constexpr int kMergeWaves = 8;
 constexpr int kMergeThreads = kMergeWaves * kWave;
 constexpr int kSearches = 4;                  // binary searches of a thread in flight
+constexpr int kMergeBlocks = 1 << 16;         // merging workgroups, at most (the chip holds 1024)
 constexpr int kFillBlocks = 1 << 16;          // zero-filling workgroups per launch, at most
 constexpr int kReduceThreads = 256;
 constexpr int kMaxPer = 8;                    // tokens that a lane group adds up alone
@@ -540,68 +541,71 @@ struct MergeParams {
   int fan;         // runs that make one
   const int32_t *key_in, *pos_in;
   int32_t *key_out, *pos_out;
-  int64_t blocks;  // of tokens
+  int blocks;      // merging workgroups; further ones fill
 };
 
-// A workgroup places 64 neighbouring tokens of one run: each of its waves
-// searches for them in every kMergeWaves-th run, kSearches runs at a time, so
-// that few steps wait for one another, and the waves' counts are added.
+// A workgroup places 64 neighbouring tokens of one run at a time: each of its
+// waves searches for them in every kMergeWaves-th run, kSearches runs at a time,
+// so that few steps wait for one another, and the waves' counts are added.
 __global__ __launch_bounds__(kMergeThreads) void merge_kernel(MergeParams p, Fill fill) {
-  if ((int64_t)blockIdx.x >= p.blocks) {
-    fill_part(fill, (int)(blockIdx.x - p.blocks));
+  if ((int)blockIdx.x >= p.blocks) {
+    fill_part(fill, (int)blockIdx.x - p.blocks);
     return;
   }
   __shared__ int32_t counts[kMergeWaves][kWave];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t i0 = (int64_t)blockIdx.x * kWave;  // (a run is a multiple of 64)
-  const bool there = i0 + lane < p.n;
   const int64_t run = p.run, span = run * p.fan;
-  const int64_t base = i0 / span * span;
-  const int mine = (int)((i0 - base) / run);
-  const int32_t key = there ? p.key_in[i0 + lane] : 0;
-  const int64_t left = (p.n - base + run - 1) / run;
-  const int fan = left < p.fan ? (int)left : p.fan;
   uint32_t top = 1;
   while ((int64_t)top * 2 <= run) top *= 2;
-  uint32_t before = 0;
-  for (int q0 = wave; q0 < fan; q0 += kSearches * kMergeWaves) {
-    // tokens of run q that come before this one: those of lower rows, and in
-    // the runs before its own those of its row too
-    const char *a[kSearches];
-    uint32_t len[kSearches], at[kSearches];
-    int32_t limit[kSearches];
+  // (a run is a multiple of 64)
+  for (int64_t i0 = (int64_t)blockIdx.x * kWave; i0 < p.n; i0 += (int64_t)p.blocks * kWave) {
+    const bool there = i0 + lane < p.n;
+    const int64_t base = i0 / span * span;
+    const int mine = (int)((i0 - base) / run);
+    const int32_t key = there ? p.key_in[i0 + lane] : 0;
+    const int64_t left = (p.n - base + run - 1) / run;
+    const int fan = left < p.fan ? (int)left : p.fan;
+    uint32_t before = 0;
+    for (int q0 = wave; q0 < fan; q0 += kSearches * kMergeWaves) {
+      // tokens of run q that come before this one: those of lower rows, and in
+      // the runs before its own those of its row too
+      const char *a[kSearches];
+      uint32_t len[kSearches], at[kSearches];
+      int32_t limit[kSearches];
 #pragma unroll
-    for (int u = 0; u < kSearches; ++u) {
-      const int q = q0 + u * kMergeWaves;
-      const bool search = q < fan && q != mine;
-      const int64_t start = base + (search ? q : 0) * run;
-      a[u] = (const char *)(p.key_in + start);
-      len[u] = search ? (uint32_t)(p.n - start < run ? p.n - start : run) : 0;
-      limit[u] = key + (q < mine ? 1 : 0);
-      at[u] = 0;
+      for (int u = 0; u < kSearches; ++u) {
+        const int q = q0 + u * kMergeWaves;
+        const bool search = q < fan && q != mine;
+        const int64_t start = base + (search ? q : 0) * run;
+        a[u] = (const char *)(p.key_in + start);
+        len[u] = search ? (uint32_t)(p.n - start < run ? p.n - start : run) : 0;
+        limit[u] = key + (q < mine ? 1 : 0);
+        at[u] = 0;
+      }
+      for (uint32_t s = top; s > 0; s >>= 1) {
+        int32_t got[kSearches];
+#pragma unroll
+        for (int u = 0; u < kSearches; ++u)
+          if (len[u] > 0)  // (index 0: in range, not used)
+            got[u] = *(const int32_t *)(a[u] + (at[u] + s <= len[u] ? at[u] + s - 1 : 0u) * 4u);
+#pragma unroll
+        for (int u = 0; u < kSearches; ++u)
+          if (len[u] > 0) at[u] += at[u] + s <= len[u] && got[u] < limit[u] ? s : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kSearches; ++u) before += at[u];
     }
-    for (uint32_t s = top; s > 0; s >>= 1) {
-      int32_t got[kSearches];
+    counts[wave][lane] = (int32_t)before;
+    __syncthreads();
+    if (wave == 0 && there) {
+      int64_t to = i0 + lane - mine * run;  // base and the place in its own run
 #pragma unroll
-      for (int u = 0; u < kSearches; ++u)
-        if (len[u] > 0)  // (index 0: in range, not used)
-          got[u] = *(const int32_t *)(a[u] + (at[u] + s <= len[u] ? at[u] + s - 1 : 0u) * 4u);
-#pragma unroll
-      for (int u = 0; u < kSearches; ++u)
-        if (len[u] > 0) at[u] += at[u] + s <= len[u] && got[u] < limit[u] ? s : 0;
+      for (int w = 0; w < kMergeWaves; ++w) to += counts[w][lane];
+      p.key_out[to] = key;
+      p.pos_out[to] = p.pos_in[i0 + lane];
     }
-#pragma unroll
-    for (int u = 0; u < kSearches; ++u) before += at[u];
-  }
-  counts[wave][lane] = (int32_t)before;
-  __syncthreads();
-  if (wave == 0 && there) {
-    int64_t to = i0 + lane - mine * run;  // base and the place in its own run
-#pragma unroll
-    for (int w = 0; w < kMergeWaves; ++w) to += counts[w][lane];
-    p.key_out[to] = key;
-    p.pos_out[to] = p.pos_in[i0 + lane];
+    __syncthreads();  // counts are read before the next tokens' are written
   }
 }
 
@@ -875,7 +879,8 @@ hipError_t launch_typed(const GradParams &g, void *ws, hipStream_t stream) {
   m.n = g.n;
   m.run = kTile;
   m.fan = l.fan;
-  m.blocks = (g.n + kWave - 1) / kWave;
+  const int64_t groups = (g.n + kWave - 1) / kWave;
+  m.blocks = (int)(groups < kMergeBlocks ? groups : kMergeBlocks);
   for (int level = 0; level < l.levels; ++level) {
     m.key_in = (const int32_t *)(w + l.key[level & 1]);
     m.pos_in = (const int32_t *)(w + l.pos[level & 1]);

@@ -869,12 +869,15 @@ hipError_t launch_typed(const GradParams &g, void *ws, hipStream_t stream) {
   const int tiles = (int)((g.n + kTile - 1) / kTile);
   Fill f = part_of(g, ob, 0, fills, kThreads);
   const dim3 grid((unsigned)(tiles + f.blocks)), block(kThreads);
+  // each launch reads what the one before wrote: none follows one that failed
+  hipError_t err;
   if (g.rows < kRows32<kMany>)
     launch_kernel(tile_sort_kernel<uint32_t>, grid, block, 0, stream, g.token, g.n, g.rows, tiles,
                   key, pos, f);
   else
     launch_kernel(tile_sort_kernel<uint64_t>, grid, block, 0, stream, g.token, g.n, g.rows, tiles,
                   key, pos, f);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
   MergeParams m{};
   m.n = g.n;
   m.run = kTile;
@@ -889,6 +892,7 @@ hipError_t launch_typed(const GradParams &g, void *ws, hipStream_t stream) {
     f = part_of(g, ob, 1 + level, fills, kMergeThreads);
     launch_kernel(merge_kernel, dim3((unsigned)(m.blocks + f.blocks)), dim3(kMergeThreads), 0,
                   stream, m, f);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
     m.run *= l.fan;
   }
   ReduceParams rp{};
@@ -909,6 +913,7 @@ hipError_t launch_typed(const GradParams &g, void *ws, hipStream_t stream) {
     launch_kernel(reduce_kernel<TG, TO, 4>, reduce_grid, dim3(kReduceThreads), 0, stream, rp);
   else
     launch_kernel(reduce_kernel<TG, TO, 2>, reduce_grid, dim3(kReduceThreads), 0, stream, rp);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t blocks = l.parts * l.slices < kMaxBlocks ? l.parts : kMaxBlocks / l.slices;
   launch_kernel(fix_kernel<TO>, dim3((unsigned)blocks, l.slices), dim3(kFixThreads), 0, stream, rp);
   return hipGetLastError();

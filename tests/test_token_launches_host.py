@@ -127,6 +127,18 @@ def test_gradient_launches_hold_fewer_than_2_to_32_threads(launches):
     _check(launches, calls)
 
 
+def test_gradient_stops_at_a_launch_that_failed(launches):
+    """What follows reads what it should have written."""
+    for n in (100, 5000, 100_000, 5_000_000):
+        whole = _grad(n, 1000, 8, 0, 8)
+        (status, made), = launches([whole])
+        assert status == OK
+        calls = [_grad(n, 1000, 8, 0, 8, fail=i) for i in range(len(made))]
+        for i, (status, first) in enumerate(launches(calls)):
+            assert status == HIP, (n, i)
+            assert first == made[:i + 1], (n, i)
+
+
 def test_other_launches_hold_fewer_than_2_to_32_threads(launches):
     calls = []
     for n in (1, 1000, 1 << 20, (1 << 28) + 1, INT32_MAX):

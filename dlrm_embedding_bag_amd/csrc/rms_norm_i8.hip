@@ -72,6 +72,9 @@ __device__ __forceinline__ void row_reduce(double &ss, double &mx, double *sh, i
 // Products h * weight between this and its inverse are rounded to float32, and
 // scaled, without leaving its normal range (beyond it a product overflows).
 constexpr double kLeast = 0x1p-100;
+// float32's least normal value: a scale below it has fewer than 24 bits, and
+// max|y| / scale may lie well beyond 127.
+constexpr float kLeastScale = 0x1p-126f;
 
 // 1 / sqrt(d) and 1 / d in float64: the hardware's estimate and two steps of
 // Newton's iteration, each of which doubles its digits (24 at least).  Every
@@ -105,7 +108,7 @@ __device__ __forceinline__ RowScale row_scale(double ss, double mx, int dim, dou
   RowScale o;
   o.s = (float)(mx * r * (1.0 / 127.0));
   o.f = (o.s > 0.0f && o.s < INFINITY) ? r * inverse((double)o.s) : 0.0;
-  o.f32 = mx > kLeast && mx < 1.0 / kLeast ? (float)o.f : 0.0f;
+  o.f32 = mx > kLeast && mx < 1.0 / kLeast && o.s >= kLeastScale ? (float)o.f : 0.0f;
   return o;
 }
 
@@ -117,9 +120,11 @@ __device__ __forceinline__ int code(float h, float w, double f) {
 __device__ __forceinline__ void store_codes(int8_t *row, int c, int dim, const float (&h)[8],
                                             const float (&w)[8], const RowScale &rs) {
   // Added to 1.5 * 2^23 a value is rounded to a whole number (ties to even),
-  // whose low byte is the code.  h * w and f32 are each off by at most 2^-24 of
-  // a value of at most 127: where that lies 2^-14 or more from a border, the
-  // exact one lies on the same side, and both round to the same code.
+  // whose low byte is the code.  Values are at most 127 but for the scale's
+  // rounding, 127 * 2^-24 (f32 is zero where a scale has fewer bits).  h * w and
+  // f32 are each off by at most 2^-24 of that: where a value lies 2^-14 or more
+  // from a border, the exact one lies on the same side, and both round to the
+  // same code.
   constexpr float kWhole = 12582912.0f;
   uint32_t q[8];
   bool clear = rs.f32 != 0.0f;

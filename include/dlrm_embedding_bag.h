@@ -647,8 +647,9 @@ DLRM_API int rms_norm_residual_i8(int64_t m, int32_t dim, const void *x, int64_t
  * each row of a (token) and of w (channel):
  *   c[m, n] = act(bias[n] + a_scale[m] w_scale[n] sum_k a[m, k] w[n, k])
  * The sum over k is exact; it is rounded to float32, scaled, and the result
- * rounded once to out_dtype.  A NaN scale leaves NaN in its row or column,
- * through every act.
+ * rounded once to out_dtype.  The scales' product may leave float32's range
+ * where the result does not (or where the sum is zero).  A NaN scale leaves NaN
+ * in its row or column, through every act.
  *
  *   m >= 0 (0: nothing to do), n >= 1, 1 <= k <= 131071 (beyond it the int32
  *   sum could overflow: DLRM_ERR_UNSUPPORTED, as for m or n above 2^26)

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from conftest import gpu_available
-from test_token_ops_gpu import TINY, U32, _check_grad, _draw_tokens, _dt, _np64
+from test_token_ops_gpu import TINY, U, U32, _check_grad, _draw_tokens, _dt, _np64
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs an MI355X GPU")]
@@ -72,3 +72,65 @@ def test_norm_scale_below_float32s_normal_range(m, dim, dtype):
         assert np.all(np.abs(_np64(s) - top) <= np.maximum(2.0 ** -150, top * U32) * 1.01)
         assert np.any((_np64(s) > 0) & (_np64(s) < TINY))
         _check_codes(q, v)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(1, 70, 4096), (30, 8200, 300), (64, 130, 2049),    # few rows
+                                   (100, 129, 2050), (2000, 2100, 273),                # any byte
+                                   (200, 150, 1024), (2000, 2100, 272), (3000, 3100, 464)])
+def test_product_of_scales_beyond_float32(m, n, k, out):
+    """a_scale * w_scale leaves float32's normal range, upwards or downwards, and
+    the outputs do not: their errors are those of other scales.  A sum of zero
+    takes no overflow from its scales."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(m + n + k)
+    a = rng.integers(-128, 128, (m, k)).astype(np.int8)
+    w = rng.integers(-128, 128, (n, k)).astype(np.int8)
+    a[m // 2] = 0
+    sizes_a = np.array([1e-22, 1e25, 1e-3, 0.0, 1e-38, 3e-44, 1e30])
+    sizes_w = np.array([1e-20, 1e-3, 1e20, -1e-5, 0.0])
+    sa = (sizes_a[np.arange(m) % 7] * (1 + rng.random(m))).astype(np.float32)
+    sw = (sizes_w[np.arange(n) % 5] * (1 + rng.random(n))).astype(np.float32)
+    sa[m // 2] = 1e30
+    b = (rng.standard_normal(n) * 1e-30).astype(np.float32)
+    ta, tw, tsa, tsw, tb = [torch.from_numpy(v).cuda() for v in (a, w, sa, sw, b)]
+    # (whole numbers below 2^31: a float64 product on the GPU is exact)
+    sums = (ta.double() @ tw.double().t()).cpu().numpy()
+    p = sums * (sa.astype(np.float64)[:, None] * sw.astype(np.float64)[None, :])
+    for bias in (None, tb):
+        c = p + (0.0 if bias is None else b.astype(np.float64))
+        got = _np64(fw.linear_i8_bias_act(ta, tsa, tw, tsw, bias, out_dtype=_dt(out)))
+        high = np.abs(c) >= 2.0 ** 128
+        assert np.array_equal(got[high], np.sign(c[high]) * np.inf)
+        tol = (3 * np.abs(p) + np.abs(c)) * U32 * 1.01
+        tol = tol * (1 + U[out]) + np.abs(c) * U[out] * 1.01 * (out == "bf16") + TINY
+        bad = ~high & ~(np.abs(got - c) <= tol)
+        assert not bad.any(), (f"{bad.sum()} of {bad.size} off, first at {tuple(np.argwhere(bad)[0])}: "
+                               f"{got[bad][0]!r} for {c[bad][0]!r}")
+        assert np.array_equal(got[m // 2], np.zeros(n) if bias is None else
+                              _np64(bias.to(_dt(out))))
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 70, 300), (100, 129, 330), (200, 150, 1024),
+                                   (2000, 2100, 272), (3000, 3100, 464), (2900, 3333, 321)])
+def test_product_rows_do_not_see_their_neighbours_scales(m, n, k):
+    """Equal bits of a row, whatever the scales of the rows around it."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    g = torch.Generator(device="cuda").manual_seed(m)
+    a = torch.randint(-128, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    sa = torch.rand(m, generator=g, device="cuda") * 0.01
+    sw = torch.rand(n, generator=g, device="cuda") * 1e-3
+    want = fw.linear_i8_bias_act(a, sa, w, sw, act="relu")
+    other = sa.clone()
+    other[::3] = 0.0
+    other[1::9] = 1e36
+    other[4::9] = float("nan")
+    keep = other == sa
+    got = fw.linear_i8_bias_act(a, other, w, sw, act="relu")
+    assert torch.equal(got[keep], want[keep])
+    assert torch.all(got[::3] == 0) and torch.isnan(got[4::9]).all()

@@ -134,3 +134,47 @@ def test_product_rows_do_not_see_their_neighbours_scales(m, n, k):
     got = fw.linear_i8_bias_act(a, other, w, sw, act="relu")
     assert torch.equal(got[keep], want[keep])
     assert torch.all(got[::3] == 0) and torch.isnan(got[4::9]).all()
+
+
+def _row_next_to_borders(dim, dtype, seed):
+    """A row and weights whose y / scale lies next to k + 1/2 for all codes k: the
+    weight that meets a value is the float32 next to where the border would be,
+    so the distances are of the size of float32's steps, 1e-9 to 1e-5."""
+    import torch
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy((1 + rng.random((1, dim))).astype(np.float32)).to(_dt(dtype))
+    h = _np64(x)[0]
+    w = np.ones(dim, np.float32)
+    w[0] = 200.0 / h[0]                       # the largest product
+    r = 1.0 / np.sqrt((h * h).mean() + 1e-6)
+    scale = float(np.float32(h[0] * np.float64(w[0]) * r / 127.0))
+    k = rng.integers(-127, 127, dim - 1)
+    w[1:] = ((k + 0.5) * scale / r / h[1:]).astype(np.float32)
+    return x, torch.from_numpy(w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,dim", [(1, 31), (600, 60), (600, 130), (1, 250), (1, 500), (600, 1000),
+                                   (1, 2000), (600, 2000), (1, 4000), (600, 4000), (2, 8000),
+                                   (2, 9001)])
+def test_norm_codes_next_to_borders(m, dim, dtype):
+    """Each code is the one that 64 bits decide, which float32 does not tell."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    told = 0
+    for seed in range(4):
+        x, w = _row_next_to_borders(dim, dtype, seed)
+        _, q, s = fw.rms_norm_residual_i8(x.cuda().expand(m, dim), w.cuda(), eps=1e-6)
+        _, v = _codes_of(x, w, 1e-6, s[:1])
+        away = np.abs(np.abs(v - np.floor(v)) - 0.5)
+        assert np.median(away[0, 1:]) < 1e-5
+        # the same in float32: product, factor, rounded product
+        d = _np64(x)
+        f = np.float32(1.0 / np.sqrt((d * d).mean() + 1e-6) / float(s[0]))
+        rough = np.rint((x.float().numpy() * w.numpy()).astype(np.float64) * np.float64(f))
+        told += int((rough != np.rint(v)).sum())
+        for i in {0, m // 2, m - 1}:
+            _check_codes(q[i:i + 1], v)
+        assert torch.equal(q, q[:1].expand(m, dim)) and torch.equal(s, s[:1].expand(m))
+    assert told > 0, "float32 alone would do for these inputs"

@@ -178,3 +178,29 @@ def test_norm_codes_next_to_borders(m, dim, dtype):
             _check_codes(q[i:i + 1], v)
         assert torch.equal(q, q[:1].expand(m, dim)) and torch.equal(s, s[:1].expand(m))
     assert told > 0, "float32 alone would do for these inputs"
+
+
+@pytest.mark.parametrize("kind", ["hot", "same", "uniform"])
+@pytest.mark.parametrize("n,rows,dim", [
+    (2047, 900, 33), (2048, 900, 33), (2048, 20, 1040), (2049, 900, 33),   # one launch's last
+    (1024, 4_194_303, 3), (1024, 4_194_304, 3),      # few tokens: rows of 32-bit values and beyond
+    (1025, 2_097_151, 3), (1025, 2_097_152, 3), (2048, 3_000_000, 3),      # many tokens, likewise
+    (2049, 2_097_151, 3), (2049, 2_097_152, 3),      # tiles, likewise
+    (65536, 2_097_152, 2), (65537, 2_097_151, 2)])   # one merge's last, and two
+def test_grad_at_the_sorts_own_borders(n, rows, dim, kind):
+    """Up to 2048 tokens take one launch and 32 tiles of 2048 one merge; rows below
+    2^22 (up to 1024 tokens) or 2^21 (beyond) sort as 32-bit values."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(n)
+    tok = _draw_tokens(rng, n, rows, kind)
+    if kind == "uniform":
+        tok[::7] = rows - 1
+        tok[5::97] = rows
+    g = rng.standard_normal((n, dim)).astype(np.float32)
+    td, gd = torch.from_numpy(tok).cuda(), torch.from_numpy(g).cuda()
+    got = fw.emb_lookup_grad(gd, td, rows)
+    named = _check_grad(got, g.astype(np.float64), tok, rows, 1.0, "f32")
+    assert not got.cpu()[torch.from_numpy(~named)].any()
+    assert torch.equal(got, fw.emb_lookup_grad(gd, td, rows))

@@ -158,3 +158,18 @@ def test_other_launches_hold_fewer_than_2_to_32_threads(launches):
                     calls.append(["linear_i8_bias_act", [m, n, k, FAKE, k, FAKE, FAKE, k, FAKE,
                                                          None, 0, FAKE, n, BF16, None], -1])
     _check(launches, calls)
+
+
+def test_gradient_takes_one_launch_up_to_2048_tokens(launches):
+    """and one merge up to 32 tiles of 2048; the workspace begins with the tiles."""
+    def made(n):
+        (status, all_launches), = launches([_grad(n, 1000, 8, 0, 8)])
+        assert status == OK
+        return len(all_launches)
+
+    bytes_of = abi.load().emb_lookup_grad_workspace_bytes
+    assert made(2048) == 1 and bytes_of(2048, 1000, 8) == 0
+    assert made(2049) == 4 and bytes_of(2049, 1000, 8) > 0      # sort, merge, reduce, fix
+    assert made(65536) == 4
+    assert made(65537) == 5
+    assert made(2_500_001) == 6                                 # three merges

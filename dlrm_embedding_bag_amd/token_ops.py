@@ -5,6 +5,12 @@ Argument marshalling only, as in abi.py: every function has the name of the C
 entry point it calls (include/dlrm_embedding_bag.h says what it computes),
 checks its tensors, allocates the outputs and workspace that it is not given
 on the stream the call runs on, and raises on refusal.  There is no CPU path.
+
+They work on the tensors' memory and record no graph for autograd: an output
+does not require a gradient, whatever the inputs do, and a table's gradient is
+what emb_lookup_grad gives for the rows' gradient.  A tensor given as an output
+counts as modified in place, so autograd refuses to use a value of it that was
+saved before.
 """
 from __future__ import annotations
 
@@ -127,7 +133,8 @@ def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream
     dev = _device(torch, table, "table")
     rows, dim, ld = _rows(torch, table, "table", _TABLES, dev)
     n = _tokens(torch, tokens, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         if out_dtype is None:
             out_dtype = table.dtype if table.dtype in _FLOATS else torch.float32
         out = _new(torch, (n, dim), table, stream, _out_dtype(out_dtype))
@@ -143,6 +150,8 @@ def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream
                                    _CODES[out.dtype], _handle(torch, stream, dev))
     if status:
         _check(status, "emb_lookup_scaled")
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out
 
 
@@ -167,7 +176,8 @@ def emb_lookup_grad(grad, tokens, rows=None, scale=1.0, out_dtype=None, out=None
     n = _tokens(torch, tokens, dev)
     dim = grad.shape[-1]
     ld = _token_rows(torch, grad, "grad", tokens, dim, _FLOATS, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         if accumulate:
             raise ValueError("accumulate needs out")
         if rows is None:
@@ -198,6 +208,8 @@ def emb_lookup_grad(grad, tokens, rows=None, scale=1.0, out_dtype=None, out=None
                                  _handle(torch, stream, dev))
     if status:
         _check(status, "emb_lookup_grad")
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out
 
 
@@ -211,6 +223,7 @@ def rms_norm_residual_i8(x, weight=None, residual=None, eps=1e-6, out_h=None, ou
     dev = _device(torch, x, "x")
     m, dim, ldx = _rows(torch, x, "x", _FLOATS, dev)
     dtype = x.dtype
+    given = [t for t in (out_h, out_codes, out_scale) if t is not None]
     wp = None if weight is None else _vector(torch, weight, "weight", dim, dev)
     rp, ldr, hp, ldh = None, 0, None, 0
     if residual is None:
@@ -245,6 +258,8 @@ def rms_norm_residual_i8(x, weight=None, residual=None, eps=1e-6, out_h=None, ou
                                       _handle(torch, stream, dev))
     if status:
         _check(status, "rms_norm_residual_i8")
+    if given:
+        torch.autograd.graph.increment_version(given)
     return h, out_codes, out_scale
 
 
@@ -263,7 +278,8 @@ def linear_i8_bias_act(a, a_scale, w, w_scale, bias=None, act="none", out_dtype=
     ap = _vector(torch, a_scale, "a_scale", m, dev)
     wp = _vector(torch, w_scale, "w_scale", n, dev)
     bp = None if bias is None else _vector(torch, bias, "bias", n, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new(torch, (m, n), a, stream,
                    torch.float32 if out_dtype is None else _out_dtype(out_dtype))
         ldc = n
@@ -279,4 +295,6 @@ def linear_i8_bias_act(a, a_scale, w, w_scale, bias=None, act="none", out_dtype=
                                     _handle(torch, stream, dev))
     if status:
         _check(status, "linear_i8_bias_act")
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out

@@ -204,3 +204,38 @@ def test_grad_at_the_sorts_own_borders(n, rows, dim, kind):
     named = _check_grad(got, g.astype(np.float64), tok, rows, 1.0, "f32")
     assert not got.cpu()[torch.from_numpy(~named)].any()
     assert torch.equal(got, fw.emb_lookup_grad(gd, td, rows))
+
+
+def test_given_outputs_count_as_modified():
+    """A value that autograd saved is not used after a call wrote over it; outputs
+    and tensors that were only read keep their versions."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    leaf = torch.randn(30, 16, device="cuda", requires_grad=True)
+    table = leaf * 1.0
+    tok = torch.arange(20, dtype=torch.int32, device="cuda")
+    grad = torch.randn(20, 16, device="cuda")
+    loss = table.square().sum()                      # saves table
+    before = table._version
+    rows = fw.emb_lookup_scaled(table, tok)
+    assert not rows.requires_grad and table._version == before
+    fw.emb_lookup_grad(grad, tok, out=table.detach(), accumulate=True)
+    assert table._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    codes = torch.zeros(20, 16, dtype=torch.int8, device="cuda")
+    scale, h = torch.zeros(20, device="cuda"), torch.zeros(20, 16, device="cuda")
+    y = torch.zeros(20, 8, device="cuda")
+    w = torch.ones(8, 16, dtype=torch.int8, device="cuda")
+    ws = torch.ones(8, device="cuda")
+    reads = [grad, tok, rows, w, ws]
+    versions = [t._version for t in reads]
+    fw.rms_norm_residual_i8(rows, None, grad, out_h=h, out_codes=codes, out_scale=scale)
+    fw.linear_i8_bias_act(codes, scale, w, ws, out=y)
+    lookup = torch.zeros(20, 16, device="cuda")
+    fw.emb_lookup_scaled(table, tok, out=lookup)
+    assert all(t._version == 1 for t in (h, codes, scale, y, lookup))
+    assert [t._version for t in reads] == versions
+    with torch.inference_mode():                     # tensors without a version
+        fw.emb_lookup_scaled(table, tok, out=torch.zeros(20, 16, device="cuda"))

@@ -142,6 +142,7 @@ def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream
             out = out.view(*tokens.shape, dim)
         ld_out = dim
     else:
+        _on(torch, out, "out", dev)
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out and out_dtype disagree")
         ld_out = _token_rows(torch, out, "out", tokens, dim, _FLOATS, dev)

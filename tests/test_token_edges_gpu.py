@@ -239,3 +239,23 @@ def test_given_outputs_count_as_modified():
     assert [t._version for t in reads] == versions
     with torch.inference_mode():                     # tensors without a version
         fw.emb_lookup_scaled(table, tok, out=torch.zeros(20, 16, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [None, "f32"])
+def test_outputs_that_are_not_gpu_tensors_are_refused(dtype):
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    table = torch.zeros(5, 8, device="cuda")
+    tok = torch.zeros(3, dtype=torch.int32, device="cuda")
+    codes, scale = table.to(torch.int8), torch.ones(5, device="cuda")
+    kind = {} if dtype is None else {"out_dtype": _dt(dtype)}
+    for out, error in (([0.0], TypeError), (torch.zeros(3, 8), ValueError)):
+        with pytest.raises(error, match="out must be"):
+            fw.emb_lookup_scaled(table, tok, out=out, **kind)
+        with pytest.raises(error, match="out must be"):
+            fw.emb_lookup_grad(table[:3], tok, out=out, **kind)
+        with pytest.raises(error, match="out must be"):
+            fw.linear_i8_bias_act(codes, scale, codes, scale, out=out, **kind)
+        with pytest.raises(error, match="out_h must be"):
+            fw.rms_norm_residual_i8(table, None, table, out_h=out)

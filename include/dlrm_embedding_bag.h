@@ -620,11 +620,12 @@ DLRM_API int emb_lookup_grad(int64_t num_tokens, int64_t rows, int32_t dim, cons
  *   h = x + residual, rounded to dtype      (h = x without a residual)
  *   y = h * weight / sqrt(mean(h^2) + eps)  (float64)
  *   scale = max|y| / 127                    (rounded to float32)
- *   codes = round(y / scale)                (ties to even, within +-127)
+ *   codes = round(y / scale)                (ties to even, at most 127 either way)
  * so codes * scale stands for y.  A row of zeros has scale 0 and codes 0
  * (with eps 0 it has no norm: scale NaN).  A row that holds an infinity or a
  * NaN, or that meets a weight that does, has scale NaN and codes 0; other
- * rows are not affected.
+ * rows are not affected.  Where max|y| / 127 is rounded to infinity or to zero
+ * codes are 0.
  *
  *   m >= 0 (0: nothing to do), 1 <= dim <= DLRM_MAX_TOKEN_DIM
  *   x, residual  (m, dim) of dtype (float32, bfloat16), row strides ldx, ldr;

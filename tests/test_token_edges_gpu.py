@@ -259,3 +259,70 @@ def test_outputs_that_are_not_gpu_tensors_are_refused(dtype):
             fw.linear_i8_bias_act(codes, scale, codes, scale, out=out, **kind)
         with pytest.raises(error, match="out_h must be"):
             fw.rms_norm_residual_i8(table, None, table, out_h=out)
+
+
+@pytest.mark.parametrize("dim", [40_001, 1 << 20])
+@pytest.mark.parametrize("n", [7, 2049])
+def test_lookup_and_gradient_of_the_widest_rows(n, dim):
+    """Whole numbers whose products and sums float32 holds: equal to any order's."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rows = 3
+    g = torch.Generator(device="cuda").manual_seed(n)
+    table = torch.randint(-50, 51, (rows, dim), generator=g, device="cuda").float()
+    tok = torch.randint(-1, rows + 1, (n,), generator=g, device="cuda", dtype=torch.int32)
+    few = tok[:7].contiguous()
+    there = ((few >= 0) & (few < rows))[:, None]
+    got = fw.emb_lookup_scaled(table, few, 2.0)
+    assert torch.equal(got, torch.where(there, table[few.clamp(0, rows - 1).long()] * 2.0, 0.0))
+    # one gradient row for all tokens
+    row = torch.randint(-9, 10, (1, dim), generator=g, device="cuda").float()
+    count = torch.stack([(tok == r).sum() for r in range(rows)])[:, None].float()
+    got = fw.emb_lookup_grad(row.expand(n, dim), tok, rows, scale=0.5)
+    assert torch.equal(got, count * row * 0.5)
+    want = table - count * row
+    assert torch.equal(fw.emb_lookup_grad(row.expand(n, dim), tok, scale=-1.0, out=table,
+                                          accumulate=True), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_the_widest_rows(dtype):
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    rng = np.random.default_rng(20)
+    dim = 1 << 20
+    x = torch.from_numpy(rng.standard_normal((2, dim)).astype(np.float32)).to(_dt(dtype))
+    w = torch.from_numpy((1 + 0.1 * rng.standard_normal(dim)).astype(np.float32))
+    _, q, s = fw.rms_norm_residual_i8(x.cuda(), w.cuda(), eps=1e-6)
+    y, v = _codes_of(x, w, 1e-6, s)
+    top = np.abs(y).max(1) / 127.0
+    assert np.all(np.abs(_np64(s) - top) <= top * U32 * 1.01)
+    _check_codes(q, v, border=1e-9)     # sums of 2^20 squares: 2^20 2^-53 of 127 at most
+    # a scale beyond float32: no codes (one value whose norm is 1024, a weight of 1e38)
+    x = torch.zeros(1, dim)
+    x[0, 5] = 1.0
+    w = torch.full((dim,), 1e38)
+    _, q, s = fw.rms_norm_residual_i8(x.cuda(), w.cuda(), eps=0.0)
+    assert torch.isinf(s).all() and not q.any()
+
+
+@pytest.mark.parametrize("dim,rows", [(1, 1 << 27), (300, 1 << 23), (1030, 1 << 22), (4097, 1 << 21)])
+def test_norm_of_more_rows_than_one_launch_has_workgroups_for(dim, rows):
+    """Workgroups that take a second turn: rows of a few lanes, a wave, two, eight."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    m = rows + 1001
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    base = torch.randn(977, dim, generator=g, device="cuda").bfloat16()
+    x = torch.empty(m, dim, dtype=torch.bfloat16, device="cuda")
+    whole = m // 977 * 977
+    x[:whole].view(-1, 977, dim).copy_(base[None])
+    x[whole:] = base[:m - whole]
+    _, q, s = fw.rms_norm_residual_i8(x)
+    _, q1, s1 = fw.rms_norm_residual_i8(base)
+    assert torch.equal(q[:whole].view(-1, 977, dim), q1.expand(whole // 977, 977, dim))
+    assert torch.equal(s[:whole].view(-1, 977), s1.expand(whole // 977, 977))
+    assert torch.equal(q[whole:], q1[:m - whole]) and torch.equal(s[whole:], s1[:m - whole])

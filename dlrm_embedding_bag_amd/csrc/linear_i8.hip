@@ -12,16 +12,18 @@
 // global memory takes 16-byte loads at any address.
 //
 // Three kernels, by the number of rows and the rows' alignment (launch_typed):
-//   few_rows   up to 64 rows: bound by reading W.  1 x 8192 x 8192: 13.4 us,
-//              5.0 TB/s; 32 x 8192 x 8192: 18.5 us, the rest A's 64 MB of L2
-//              reads (every CU reads all of A)
-//   staged     rows on 16 bytes.  8192^3: 440-500 us, 2.2-2.5 POP/s, where
-//              power holds the matrix cores at 1.8 GHz (all-zero operands take
-//              330 us) and they are busy 57% of the cycles; 128 x 8192 x 8192:
-//              16 us, W's bytes
-//   gemm       any rows, through registers.  2048 x 512 x 415: 6.7-7.2 us;
-//              4001 x 4099 x 4093: 181 us, bound by loads that cross 16 bytes
-//              (4096^3 from rows on 16 bytes: 63)
+//   few_rows   up to 64 rows: bound by reading W.  1 x 8192 x 8192: 13 us,
+//              5.2 TB/s; 32 x 8192 x 8192: 18 us, 64 rows 25, the rest A's
+//              reads from L2 (every workgroup reads all of A)
+//   staged     rows on 16 bytes.  8192^3: 453 us, 2.4 POP/s at 2.1 GHz, the
+//              matrix cores busy 55% of the cycles.  Power has a part in that
+//              (500 us of uniform codes under sustained load, 416 of codes within
+//              +-3, 326 of zeros), waits the other; 128 x 8192 x 8192: 16 us, W's bytes
+//   gemm       any rows, through registers.  2048 x 512 x 415: 7.2 us;
+//              4001 x 4099 x 4093: 175 us (4096^3 from rows on 16 bytes: 61): loads
+//              that cross 16 bytes, one slab of them in flight.  64 x 64 tiles
+//              walk k alone, so few tiles leave CUs idle: 2000 x 100 x 5001, 64
+//              workgroups, 21 us
 #include <math.h>
 
 #include <type_traits>
@@ -641,6 +643,10 @@ void launch_few(const LinearI8Params &p, hipStream_t stream) {
                 dim3(kFewWaves * kWave), 0, stream, p);
 }
 
+// Up to 64 rows few_rows, which is right for a few.  The tiles overtake it before
+// that: N = K = 8192 takes it 18.4 us for 32 rows and 25.9 for 64, the staged
+// kernel 15.9 for 65; of rows at any byte, N = 8192, K = 8191, it takes 40 us for 8,
+// 60 for 32 and 88 for 64, the gemm 31 for 65.
 // Tiles of 256 where they make more than half as many workgroups as CUs
 // (3000 x 3000 x 3008: 44 us, 52 with 128, 55 with 64; 1024 x 8192 x 8192, 128
 // of them: 93, 87, 96); of 128 where they make 256 (1000 x 4096 x 4096: 27 us,

@@ -15,10 +15,13 @@
 // A row is held in registers between its two uses (statistics, codes), so
 // memory is read and written once: 2 reads and 1 write of the rows' type, one
 // byte of code per element, written past the caches (4096 rows' h and codes
-// otherwise push out inputs: 110 us for 79).  Memory bounds it: 16384 rows of
-// 4096 float32 with a residual take 157 us, 5.6 TB/s; bfloat16 rows of 8192
-// take 215 us, 4.4 TB/s, their two waits for a row's sum between loads and
-// stores not all covered by the three rows that a CU holds.
+// otherwise push out inputs: 110 us for 79).  Memory bounds rows of up to 4096:
+// 16384 rows of 4096 float32 with a residual take 157 us, 5.6 TB/s, 32768 of
+// bfloat16 176 us, 5.3 TB/s.  16384 bfloat16 rows of 8192, the same bytes, take
+// 201 us, 4.7 TB/s: their waits for a row's sum between loads and stores are not
+// all covered by the three rows that a CU holds (its waves wait 73% of their
+// time).  Longer rows are read again for the codes: 8192 rows of 12288 take 243
+// us, 2.9 TB/s, of 16384 289 us, 3.3 TB/s.
 #include <math.h>
 
 #include <type_traits>

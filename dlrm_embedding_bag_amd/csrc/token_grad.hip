@@ -31,9 +31,12 @@
 // Kernel times of Zipf batches (us):    sort  merge  reduce  fix
 //   40960 x 64 f32 into 1M rows            7     11      8     5   launches and
 //     the searches' chain bound it; its 18 MB would take 4
-//   65536 x 1024 bf16, 100000 rows f32    33     42     44     6   400 MB of
+//   65536 x 1024 bf16, 100000 rows f32    34     41     44     6   400 MB of
 //     zeros behind the sort (6 TB/s), then 134 MB of gradients and 80 MB of
 //     rows (4.9 TB/s): memory bounds it, but for the merge's 13 us
+//   500000 x 16 bf16 into 500000 rows      8  2 x 66     20     9   beyond 65536
+//     tokens the merges bound it, n (fan - 1) log2(run) steps of search each;
+//     its 29 MB would take 6
 //   160 x 16 (one launch): 5; 1000 x 64: 11
 #include <type_traits>
 

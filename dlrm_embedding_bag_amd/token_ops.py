@@ -24,6 +24,7 @@ _MODULE = None
 _FLOATS = ()   # float32, bfloat16
 _TABLES = ()   # and the table's FP8
 _INT8 = ()
+_INT_MAX = 2**31 - 1  # of a C int32 argument, to which ctypes narrows without a word
 
 
 def _torch():
@@ -67,6 +68,8 @@ def _rows(torch, t, what, dtypes, dev):
     if len(shape) != 2 or (stride[1] != 1 and shape[1] != 1):
         raise ValueError(f"{what} must be 2-D with unit column stride")
     m, n = shape
+    if n > _INT_MAX:
+        raise ValueError(f"{what} has more than {_INT_MAX} columns")
     return m, n, stride[0] if m > 1 else max(n, 1)
 
 
@@ -158,7 +161,7 @@ def emb_lookup_scaled(table, tokens, scale=1.0, out_dtype=None, out=None, stream
 
 def emb_lookup_grad_workspace_bytes(num_tokens, rows, dim):
     """Bytes of workspace that emb_lookup_grad takes for these sizes."""
-    return load().emb_lookup_grad_workspace_bytes(num_tokens, rows, dim)
+    return load().emb_lookup_grad_workspace_bytes(num_tokens, rows, min(dim, _INT_MAX))
 
 
 def emb_lookup_grad(grad, tokens, rows=None, scale=1.0, out_dtype=None, out=None,
@@ -276,6 +279,8 @@ def linear_i8_bias_act(a, a_scale, w, w_scale, bias=None, act="none", out_dtype=
     n, kw, ldw = _rows(torch, w, "w", _INT8, dev)
     if kw != k:
         raise ValueError("w must be (N, K) with a's K")
+    if m > _INT_MAX or n > _INT_MAX:
+        raise ValueError(f"a or w has more than {_INT_MAX} rows")
     ap = _vector(torch, a_scale, "a_scale", m, dev)
     wp = _vector(torch, w_scale, "w_scale", n, dev)
     bp = None if bias is None else _vector(torch, bias, "bias", n, dev)

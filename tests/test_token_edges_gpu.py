@@ -326,3 +326,31 @@ def test_norm_of_more_rows_than_one_launch_has_workgroups_for(dim, rows):
     assert torch.equal(q[:whole].view(-1, 977, dim), q1.expand(whole // 977, 977, dim))
     assert torch.equal(s[:whole].view(-1, 977), s1.expand(whole // 977, 977))
     assert torch.equal(q[whole:], q1[:m - whole]) and torch.equal(s[whole:], s1[:m - whole])
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """A size that a 32-bit argument would be narrowed from, to one that is
+    accepted, is refused."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    wide, tok = (1 << 32) + 8, torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def row(dtype):
+        return torch.empty(1, wide, dtype=dtype, device="cuda")
+
+    assert fw.emb_lookup_grad_workspace_bytes(5000, 10, wide) == 0
+    with pytest.raises(ValueError, match="columns"):
+        fw.emb_lookup_scaled(row(torch.float8_e4m3fn), tok, out_dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="columns"):
+        fw.emb_lookup_grad(row(torch.bfloat16), tok, 1)
+    with pytest.raises(ValueError, match="columns"):
+        fw.rms_norm_residual_i8(row(torch.bfloat16))
+    codes, one = row(torch.int8), torch.ones(1, device="cuda")
+    with pytest.raises(ValueError, match="columns"):
+        fw.linear_i8_bias_act(codes, one, codes, one)
+    many = torch.ones(1, 16, dtype=torch.int8, device="cuda").expand(wide, 16)
+    with pytest.raises(ValueError, match="rows"):
+        fw.linear_i8_bias_act(many, one, codes[:, :16], one)
+    with pytest.raises(ValueError, match="rows"):
+        fw.linear_i8_bias_act(codes[:, :16], one, many, one)

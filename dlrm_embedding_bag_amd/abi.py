@@ -36,7 +36,9 @@ EXPORTS = ("dlrm_status_string", "dlrm_abi_version", "dlrm_set_kernel_timing_eve
            "dlrm_plan_create",
            "dlrm_plan_update", "dlrm_plan_run", "dlrm_plan_destroy",
            "emb_lookup_scaled", "emb_lookup_grad_workspace_bytes", "emb_lookup_grad",
-           "rms_norm_residual_i8", "linear_i8_bias_act")
+           "rms_norm_residual_i8", "linear_i8_bias_act",
+           "qk_norm_rope", "qk_norm_rope_grad_workspace_bytes", "qk_norm_rope_grad",
+           "attention_packed")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -151,6 +153,19 @@ def load(path: str = LIB_PATH):
     lib.linear_i8_bias_act.restype = ctypes.c_int
     lib.linear_i8_bias_act.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
                                        _i32, _vp, _i64, _i32, _vp]
+    rows = [_vp, _i64, _i64]  # (tokens, heads, dim) with strides of tokens and heads
+    lib.qk_norm_rope.restype = ctypes.c_int
+    lib.qk_norm_rope.argtypes = [_i64, _i32, _i32, _i32, _i32, *rows, *rows, _vp, _vp, _i32, _i32,
+                                 _vp, _vp, f64, *rows, *rows, _vp]
+    lib.qk_norm_rope_grad_workspace_bytes.restype = size
+    lib.qk_norm_rope_grad_workspace_bytes.argtypes = [_i64, _i32]
+    lib.qk_norm_rope_grad.restype = ctypes.c_int
+    lib.qk_norm_rope_grad.argtypes = [_i64, _i32, _i32, _i32, _i32, *rows, *rows, *rows, *rows,
+                                      _vp, _vp, _i32, _i32, _vp, _vp, f64, *rows, *rows, _vp, _vp,
+                                      _vp, size, _vp]
+    lib.attention_packed.restype = ctypes.c_int
+    lib.attention_packed.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32, _i32, *rows, *rows, *rows,
+                                     _vp, _vp, _i32, f32, _i32, *rows, _vp, _vp]
     if path == LIB_PATH:
         _LIB = lib
     return lib

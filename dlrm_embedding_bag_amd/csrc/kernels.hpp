@@ -275,4 +275,53 @@ struct LinearI8Params {
 };
 hipError_t launch_linear_i8(const LinearI8Params &p, int out_dtype, hipStream_t stream);
 
+// Norm and rotation of queries and keys (qk_norm_rope.hip).
+constexpr int kMaxRopeDim = 256;
+struct RopeSide {       // queries or keys: (tokens, heads, dim)
+  int heads;            // 0: none
+  const void *x;
+  int64_t x_token, x_head;
+  const float *weight;  // (dim,) or null
+  void *y;              // the output: rows, or the gradient of x
+  int64_t y_token, y_head;
+  const void *grad;     // of the rows (the gradient's call)
+  int64_t g_token, g_head;
+  float *dweight;       // its gradient, or null
+};
+struct RopeParams {
+  int64_t tokens;
+  int dim, pairs;
+  const int32_t *positions;  // (tokens,)
+  const float *freqs;        // (pairs,)
+  double eps;
+  RopeSide q, k;
+};
+hipError_t launch_rope(const RopeParams &p, int dtype, bool interleaved, hipStream_t stream);
+size_t rope_grad_workspace(int64_t tokens, int dim);
+hipError_t launch_rope_grad(const RopeParams &p, int dtype, bool interleaved, void *ws,
+                            hipStream_t stream);
+
+// Attention over packed sequences (attention_packed.hip, attention_grad.hip).
+struct HeadRows {  // (tokens, heads, dim), strides in elements
+  const void *data;
+  int64_t token, head;
+};
+struct HeadRowsOut {
+  void *data;
+  int64_t token, head;
+};
+struct AttentionParams {
+  int64_t tokens, kv_tokens, batch;
+  int heads, group, dim;  // group: heads for each key head
+  HeadRows q, k, v;
+  const int32_t *offsets;     // (batch + 1,)
+  const int32_t *kv_offsets;  // the same, or null: the keys' are the queries'
+  int causal;
+  float scale;
+  int fill;        // 1: zeros in out, 2: -inf in lse, for rows outside all sequences
+  HeadRowsOut out;
+  float *lse;      // (tokens, heads), or null
+};
+hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream);
+
 }  // namespace dlrm

@@ -667,6 +667,114 @@ DLRM_API int linear_i8_bias_act(int32_t m, int32_t n, int32_t k, const int8_t *a
                                 const float *w_scale, const float *bias, int32_t act, void *c,
                                 int64_t ldc, int32_t out_dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention operators: norm and rotation of query and key heads, attention
+ * over packed sequences, and their gradients.  They follow the conventions at
+ * the top of this header, and
+ *  - queries, keys, values and their gradients are (tokens, heads, dim) of
+ *    float32 or bfloat16 (`dtype`, the same for all of a call) with a stride for
+ *    tokens and one for heads, in elements, and unit stride within a head: a
+ *    slice of a joint product and either order of tokens and heads need no
+ *    copy.  Strides of an input may be 0 (one row, repeated); an output's rows
+ *    must not overlap each other;
+ *  - heads and kv_heads are at most 65536;
+ *  - arithmetic is in float32 or more; what is rounded to bfloat16 on the way
+ *    is named.
+ */
+#define DLRM_MAX_ROPE_DIM 256      /* elements of a head: norm and rotation */
+#define DLRM_MAX_ATTENTION_DIM 128 /* the same: attention */
+
+/*
+ * qk_norm_rope -- for each head's row x of q, and of k:
+ *   v = x * weight / sqrt(mean(x^2) + eps)
+ *   pair i of v, (a, b)  ->  (a cos(t f) - b sin(t f), a sin(t f) + b cos(t f))
+ * with t = positions[token] and f = freqs[i].  Pairs are elements (i, i + pairs),
+ * or (2 i, 2 i + 1) if interleaved; elements from 2 * pairs on are not turned.
+ * The mean and the angle t f are in float64, so positions may lie far out; the
+ * result is rounded once.  An infinity or a NaN in a row leaves NaN in that row
+ * only.
+ *
+ *   tokens     0 <= tokens <= INT32_MAX (0: nothing to do)
+ *   heads, kv_heads  >= 0, not both 0 (0: q or k is not used and may be NULL)
+ *   dim        a multiple of 8 up to DLRM_MAX_ROPE_DIM
+ *   pairs      a multiple of 4, 4 <= pairs <= dim / 2
+ *   positions  (tokens,) int32, any values
+ *   freqs      (pairs,) float32, angles for each position
+ *   q_weight, k_weight  (dim,) float32, or NULL for ones
+ *   eps        finite, >= 0
+ *   out_q, out_k  may be q and k themselves (same pointer and strides)
+ */
+DLRM_API int qk_norm_rope(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim,
+                          int32_t dtype, const void *q, int64_t q_token, int64_t q_head,
+                          const void *k, int64_t k_token, int64_t k_head,
+                          const int32_t *positions, const float *freqs, int32_t pairs,
+                          int32_t interleaved, const float *q_weight, const float *k_weight,
+                          double eps, void *out_q, int64_t oq_token, int64_t oq_head, void *out_k,
+                          int64_t ok_token, int64_t ok_head, void *stream);
+
+/*
+ * qk_norm_rope_grad -- the gradients of qk_norm_rope, from those of its outputs
+ * and its inputs:
+ *   out_q, out_k                gradients of q and k, rounded once; may be the
+ *                               incoming gradients or q and k themselves
+ *   out_q_weight, out_k_weight  (dim,) float32 gradients of the weights, sums
+ *                               over all tokens and heads in a fixed order, or
+ *                               NULL where they are not wanted
+ *   workspace  16-byte aligned, at least qk_norm_rope_grad_workspace_bytes(tokens,
+ *              dim) bytes (it returns 0 for sizes that the call refuses); not
+ *              used and may be NULL without gradients of weights
+ */
+DLRM_API size_t qk_norm_rope_grad_workspace_bytes(int64_t tokens, int32_t dim);
+DLRM_API int qk_norm_rope_grad(
+    int64_t tokens, int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype,
+    const void *grad_q, int64_t gq_token, int64_t gq_head, const void *grad_k, int64_t gk_token,
+    int64_t gk_head, const void *q, int64_t q_token, int64_t q_head, const void *k,
+    int64_t k_token, int64_t k_head, const int32_t *positions, const float *freqs, int32_t pairs,
+    int32_t interleaved, const float *q_weight, const float *k_weight, double eps, void *out_q,
+    int64_t oq_token, int64_t oq_head, void *out_k, int64_t ok_token, int64_t ok_head,
+    float *out_q_weight, float *out_k_weight, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
+ * attention_packed -- attention over a batch of sequences whose rows lie one
+ * after another.  Sequence b holds query rows offsets[b] .. offsets[b + 1] - 1
+ * and key rows kv_offsets[b] .. kv_offsets[b + 1] - 1.  For query row i of a
+ * sequence and a head h of key head g = h / (heads / kv_heads):
+ *   s[j]   = scale * q[i, h] . k[j, g]   for the sequence's keys j that i sees
+ *   lse    = log(sum_j exp(s[j]))
+ *   out    = sum_j exp(s[j] - lse) v[j, g]
+ * With causal the last query sees all keys, the one before it all but the last,
+ * and so on, so that a sequence with more keys than queries continues one.  A
+ * row that sees no key (or whose scores are all -inf) has out 0 and lse -inf.
+ * What a row does not see does not reach it, not as a NaN either.
+ * For bfloat16 inputs exp(s - m) of each row's running maximum m is rounded to
+ * bfloat16 before it meets the values; out is rounded once.
+ *
+ *   tokens, kv_tokens  rows of q and out, and of k and v; up to INT32_MAX
+ *   batch       sequences, 1 <= batch < INT32_MAX; sequences may be empty
+ *   heads       a multiple of kv_heads, which is >= 1
+ *   dim         a multiple of 8 (DLRM_ERR_SHAPE); beyond DLRM_MAX_ATTENTION_DIM
+ *               DLRM_ERR_UNSUPPORTED
+ *   q, k, v, out  on 16 bytes, strides of multiples of 16 bytes; token strides
+ *               of k and v up to 2^22 elements (else DLRM_ERR_UNSUPPORTED)
+ *   offsets     (batch + 1,) int32, not decreasing, within [0, tokens]
+ *   kv_offsets  the same for k and v, or NULL where they are offsets (then
+ *               kv_tokens is tokens).  Offsets that are out of order give
+ *               undefined results within the tensors
+ *   causal      0 or 1
+ *   scale       finite, > 0
+ *   fill        what becomes of rows outside all sequences: 0 they are left as
+ *               they are; + 1 they are zero in out; + 2 they are -inf in lse
+ *   lse         (tokens, heads) float32, or NULL
+ */
+DLRM_API int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t heads,
+                              int32_t kv_heads, int32_t dim, int32_t dtype, const void *q,
+                              int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
+                              int64_t k_head, const void *v, int64_t v_token, int64_t v_head,
+                              const int32_t *offsets, const int32_t *kv_offsets, int32_t causal,
+                              float scale, int32_t fill, void *out, int64_t o_token,
+                              int64_t o_head, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

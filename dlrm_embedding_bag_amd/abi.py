@@ -38,7 +38,7 @@ EXPORTS = ("dlrm_status_string", "dlrm_abi_version", "dlrm_set_kernel_timing_eve
            "emb_lookup_scaled", "emb_lookup_grad_workspace_bytes", "emb_lookup_grad",
            "rms_norm_residual_i8", "linear_i8_bias_act",
            "qk_norm_rope", "qk_norm_rope_grad_workspace_bytes", "qk_norm_rope_grad",
-           "attention_packed")
+           "attention_packed", "attention_packed_grad_workspace_bytes", "attention_packed_grad")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -166,6 +166,12 @@ def load(path: str = LIB_PATH):
     lib.attention_packed.restype = ctypes.c_int
     lib.attention_packed.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32, _i32, *rows, *rows, *rows,
                                      _vp, _vp, _i32, f32, _i32, *rows, _vp, _vp]
+    lib.attention_packed_grad_workspace_bytes.restype = size
+    lib.attention_packed_grad_workspace_bytes.argtypes = [_i64, _i32]
+    lib.attention_packed_grad.restype = ctypes.c_int
+    lib.attention_packed_grad.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32, _i32, *rows, *rows,
+                                          *rows, *rows, *rows, _vp, _vp, _vp, _i32, f32, _i32,
+                                          *rows, *rows, *rows, _vp, size, _vp]
     if path == LIB_PATH:
         _LIB = lib
     return lib

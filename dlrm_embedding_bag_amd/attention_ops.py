@@ -252,3 +252,47 @@ def attention_packed(q, k, v, offsets, kv_offsets=None, causal=True, scale=None,
         _check(status, "attention_packed")
     _mark(torch, given)
     return out, lse
+
+
+def attention_packed_grad_workspace_bytes(tokens, heads):
+    """Bytes of workspace that attention_packed_grad takes for these sizes."""
+    return load().attention_packed_grad_workspace_bytes(tokens, min(heads, _INT_MAX))
+
+
+def attention_packed_grad(grad, q, k, v, out, lse, offsets, kv_offsets=None, causal=True,
+                          scale=None, out_q=None, out_k=None, out_v=None, workspace=None,
+                          stream=None):
+    """Gradients (of q, of k, of v) of attention_packed's out, from that of out,
+    its inputs and both its outputs.  Rows outside all sequences are 0 in new
+    tensors and left as they are in given ones.  `workspace` is a uint8 tensor of
+    at least attention_packed_grad_workspace_bytes; without it one is allocated
+    for the call."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_of(torch, q, "q")
+    dev = _device(torch, q, "q")
+    sizes, rows, off, koff, scale = _packed(torch, q, k, v, offsets, kv_offsets, scale, dev, dtype)
+    n, m, _, heads, kv_heads, dim, _ = sizes
+    gn, gh, gd, gt, ghs = _heads(torch, grad, "grad", dtype, dev)
+    on, oh, od, ot, ohs = _heads(torch, out, "out", dtype, dev)
+    if (gn, gh, gd) != (n, heads, dim) or (on, oh, od) != (n, heads, dim):
+        raise ValueError("grad and out must have q's shape")
+    if not isinstance(lse, torch.Tensor) or lse.shape != (n, heads):
+        raise ValueError("lse must be (tokens, heads)")
+    lp = _vector(torch, lse, "lse", n * heads, dev)
+    given = (out_q, out_k, out_v)
+    fill = sum(1 << i for i, t in enumerate(given) if t is None)
+    out_q, qt, qh = _rows_out(torch, out_q, "out_q", (n, heads, dim), q, stream, dtype, dev)
+    out_k, kt, kh = _rows_out(torch, out_k, "out_k", (m, kv_heads, dim), q, stream, dtype, dev)
+    out_v, vt, vh = _rows_out(torch, out_v, "out_v", (m, kv_heads, dim), q, stream, dtype, dev)
+    size = lib.attention_packed_grad_workspace_bytes(n, heads)
+    ws, size, _hold = _scratch(torch, workspace, size, q, stream, dev)
+    status = lib.attention_packed_grad(*sizes, grad.data_ptr(), gt, ghs, *rows, out.data_ptr(), ot,
+                                       ohs, lp, off, koff, 1 if causal else 0, scale, fill,
+                                       out_q.data_ptr(), qt, qh, out_k.data_ptr(), kt, kh,
+                                       out_v.data_ptr(), vt, vh, ws, size,
+                                       _handle(torch, stream, dev))
+    if status:
+        _check(status, "attention_packed_grad")
+    _mark(torch, given)
+    return out_q, out_k, out_v

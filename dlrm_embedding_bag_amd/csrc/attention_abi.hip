@@ -178,4 +178,74 @@ int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t h
   return status_of(launch_attention(p, dtype, (hipStream_t)stream));
 }
 
+size_t attention_packed_grad_workspace_bytes(int64_t tokens, int32_t heads) {
+  return tokens >= 0 && tokens <= INT32_MAX && heads >= 1 && heads <= kMaxHeads
+             ? attention_grad_workspace(tokens, heads)
+             : 0;
+}
+
+int attention_packed_grad(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t heads,
+                          int32_t kv_heads, int32_t dim, int32_t dtype, const void *grad,
+                          int64_t g_token, int64_t g_head, const void *q, int64_t q_token,
+                          int64_t q_head, const void *k, int64_t k_token, int64_t k_head,
+                          const void *v, int64_t v_token, int64_t v_head, const void *out,
+                          int64_t o_token, int64_t o_head, const float *lse,
+                          const int32_t *offsets, const int32_t *kv_offsets, int32_t causal,
+                          float scale, int32_t fill, void *dq, int64_t dq_token, int64_t dq_head,
+                          void *dk, int64_t dk_token, int64_t dk_head, void *dv, int64_t dv_token,
+                          int64_t dv_head, void *workspace, size_t workspace_bytes, void *stream) {
+  const int bad =
+      attention_shape(tokens, kv_tokens, batch, heads, kv_heads, dim, dtype, causal, scale);
+  if (bad) return bad;
+  if (fill < 0 || fill > 7 || (!kv_offsets && kv_tokens != tokens)) return DLRM_ERR_SHAPE;
+  if (!in_rows(g_token, g_head) || !in_rows(q_token, q_head) || !in_rows(k_token, k_head) ||
+      !in_rows(v_token, v_head) || !in_rows(o_token, o_head))
+    return DLRM_ERR_SHAPE;
+  if (!out_rows(tokens, heads, dim, dq_token, dq_head) ||
+      !out_rows(kv_tokens, kv_heads, dim, dk_token, dk_head) ||
+      !out_rows(kv_tokens, kv_heads, dim, dv_token, dv_head))
+    return DLRM_ERR_SHAPE;
+  if (tokens == 0 && kv_tokens == 0) return DLRM_OK;
+  if (!offsets || (tokens > 0 && (!grad || !q || !out || !lse || !dq)) ||
+      (kv_tokens > 0 && (!k || !v || !dk || !dv)))
+    return DLRM_ERR_NULL;
+  if (!aligned_rows(grad, tokens, g_token, heads, g_head, dtype) ||
+      !aligned_rows(q, tokens, q_token, heads, q_head, dtype) ||
+      !aligned_rows(k, kv_tokens, k_token, kv_heads, k_head, dtype) ||
+      !aligned_rows(v, kv_tokens, v_token, kv_heads, v_head, dtype) ||
+      !aligned_rows(out, tokens, o_token, heads, o_head, dtype) ||
+      !aligned_rows(dq, tokens, dq_token, heads, dq_head, dtype) ||
+      !aligned_rows(dk, kv_tokens, dk_token, kv_heads, dk_head, dtype) ||
+      !aligned_rows(dv, kv_tokens, dv_token, kv_heads, dv_head, dtype))
+    return DLRM_ERR_UNSUPPORTED;
+  if ((kv_tokens > 1 && (k_token > kMaxTokenStride || v_token > kMaxTokenStride)) ||
+      (tokens > 1 && (q_token > kMaxTokenStride || g_token > kMaxTokenStride)))
+    return DLRM_ERR_UNSUPPORTED;
+  const size_t need = attention_grad_workspace(tokens, heads);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return DLRM_ERR_WORKSPACE;
+  AttentionGradParams p{};
+  p.tokens = tokens;
+  p.kv_tokens = kv_tokens;
+  p.batch = batch;
+  p.heads = heads;
+  p.group = heads / kv_heads;
+  p.dim = dim;
+  p.grad = {grad, tokens > 1 ? g_token : dim, g_head};
+  p.q = {q, tokens > 1 ? q_token : dim, q_head};
+  p.k = {k, kv_tokens > 1 ? k_token : dim, k_head};
+  p.v = {v, kv_tokens > 1 ? v_token : dim, v_head};
+  p.out = {out, o_token, o_head};
+  p.lse = lse;
+  p.offsets = offsets;
+  p.kv_offsets = kv_offsets;
+  p.causal = causal;
+  p.scale = scale;
+  p.fill = fill;
+  p.dq = {dq, dq_token, dq_head};
+  p.dk = {dk, dk_token, dk_head};
+  p.dv = {dv, dv_token, dv_head};
+  return status_of(launch_attention_grad(p, dtype, workspace, (hipStream_t)stream));
+}
+
 }  // extern "C"

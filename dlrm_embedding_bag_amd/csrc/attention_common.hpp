@@ -105,6 +105,21 @@ struct LdsTile {
   }
 };
 
+// `bytes` of memory from `base` on, behind which loads read zeros.  (These two
+// are no templates: the host's pass drops kernels whose templates call such
+// builtins twice.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 4 << 15);
+}
+// 16 or 4 bytes a lane, from memory to LDS: lane l's to lds[l].
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t from,
+                                            u32x4_t *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds, 16, from, 0, 0, 0);
+}
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t from, float *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds, 4, from, 0, 0, 0);
+}
+
 // What a thread asks for when a tile is filled: where its chunks lie in memory,
 // relative to the tile's first row.
 template <typename T, int ROWS, int DP, int WAVES>
@@ -131,12 +146,9 @@ struct TileLoad {
     const int n = rows < ROWS ? (int)rows : ROWS;
     const uint32_t bytes =
         n > 0 ? (uint32_t)(((n - 1) * row_stride + dim) * (int64_t)sizeof(typename T::S)) : 0;
-    const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<typename T::S *>(base), 0, bytes,
-                                                     4 << 15);
+    const auto b = buffer_of(base, bytes);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds + (i * WAVES + wave) * kWave, 16, from[i], 0,
-                                               0, 0);
+    for (int i = 0; i < LOADS; ++i) load_to_lds(b, from[i], lds + (i * WAVES + wave) * kWave);
   }
 };
 
@@ -187,6 +199,14 @@ __device__ __forceinline__ Operand<T> read_columns(const u32x4_t *lds, int r0, i
     }
   }
   return o;
+}
+
+// Loads to LDS and LDS accesses of this wave are done, and everyone's.
+__device__ __forceinline__ void landed() {
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // -------------------------------------------------------- packed sequences --
@@ -241,6 +261,45 @@ __device__ __forceinline__ Tile find_tile(const int32_t *offsets, int64_t batch,
   const int64_t k = tile - (t.first / rows + lo);
   t.row = k < 0 ? t.last : t.first + k * rows;
   return t;
+}
+
+// The keys of a tile's sequence.
+struct KeyRange {
+  int64_t first, count;
+};
+__device__ __forceinline__ KeyRange keys_of(const int32_t *offsets, const int32_t *kv_offsets,
+                                            int64_t batch, int64_t kv_tokens, const Tile &t) {
+  if (!kv_offsets) return {t.first, t.last - t.first};
+  const int64_t first = segment_start(kv_offsets, batch, kv_tokens, t.sequence + 1);
+  const int64_t last = segment_start(kv_offsets, batch, kv_tokens, t.sequence + 2);
+  return {first, last > first ? last - first : 0};
+}
+
+// How many of them, from the first on, are seen: all, or with `causal` by the
+// last row all and by each row before it one less.
+struct SeenKeys {
+  int64_t mine;      // by this lane's row
+  int64_t wave_all;  // by every row of the wave's 32
+  int64_t wave_any;  // by any of them
+  int64_t tile_any;  // by any row of the workgroup's tile
+  __device__ __forceinline__ SeenKeys(int causal, int64_t keys, int64_t last, int64_t tile_row,
+                                      int tile_rows, int wave, int64_t row, bool there) {
+    auto by = [&](int64_t r) {
+      const int64_t n = causal ? keys - (last - 1 - r) : keys;
+      return n < 0 ? 0 : n;
+    };
+    auto end = [&](int64_t r) { return r < last - 1 ? r : last - 1; };
+    const int64_t first = tile_row + wave * 32;
+    mine = there ? by(row) : 0;
+    wave_all = first + 31 < last ? by(first) : 0;
+    wave_any = first < last ? by(end(first + 31)) : 0;
+    tile_any = by(end(tile_row + tile_rows - 1));
+  }
+};
+
+// Workgroups for that many items; each takes those a grid apart.
+inline uint32_t grid_of(int64_t items) {
+  return (uint32_t)(items < (1 << 22) ? items : 1 << 22);
 }
 
 }  // namespace dlrm

@@ -1,0 +1,363 @@
+// attention_grad.hip -- the gradient of attention over packed sequences.
+//
+// With p[i, j] = exp(scale q[i] . k[j] - lse[i]), delta[i] = grad[i] . out[i] and
+//   ds[i, j] = p[i, j] (grad[i] . v[j] - delta[i])
+// over the keys that a row sees:
+//   dq[i] = scale sum_j ds[i, j] k[j]
+//   dk[j] = scale sum_i ds[i, j] q[i]     dv[j] = sum_i p[i, j] grad[i]
+// where the sums of dk and dv run over the heads that share a key head too.
+//
+// Two kernels, so that every sum has one owner and one order (no atomics): a
+// workgroup of the first owns rows and walks the keys, and leaves delta and lse
+// side by side for the second, whose workgroups own keys and walk rows and heads.
+// The scores are made twice for that: seven products of scores' size instead of
+// five.  Both keep scores transposed or not so that p and ds, made in registers,
+// are operands of the next product where they stand, as in the forward pass.
+#include <math.h>
+
+#include "attention_common.hpp"
+
+namespace dlrm {
+namespace {
+
+struct RowStats {
+  float lse2;   // of the row in units of log 2; +inf where the row sees nothing
+  float delta;
+};
+
+template <typename T, int DT>
+__device__ __forceinline__ void store_rows(typename T::S *out, const f32x16_t (&o)[DT],
+                                           float scale, int half, int dim) {
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int at = d * 32 + row_of(i, half);
+      if (at < dim) {
+        const f32x4_t w = {o[d][i] * scale, o[d][i + 1] * scale, o[d][i + 2] * scale,
+                           o[d][i + 3] * scale};
+        if constexpr (sizeof(typename T::S) == 4)
+          *reinterpret_cast<f32x4_t *>(out + at) = w;
+        else
+          *reinterpret_cast<u32x2_u *>(out + at) =
+              u32x2_u{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
+      }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float dot(const Operand<T> &a, const Operand<T> &b, float sum) {
+  if constexpr (sizeof(typename T::S) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      sum = __builtin_fmaf(a.v[e >> 2][e & 3], b.v[e >> 2][e & 3], sum);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum = __builtin_fmaf(bf16_lo(a.v[e]), bf16_lo(b.v[e]), sum);
+      sum = __builtin_fmaf(bf16_hi(a.v[e]), bf16_hi(b.v[e]), sum);
+    }
+  }
+  return sum;
+}
+
+// Rows: dq, and the rows' statistics.
+template <typename T, int DP, int WAVES, int BN>
+__global__ __launch_bounds__(WAVES *kWave) void grad_rows_kernel(AttentionGradParams p,
+                                                                 RowStats *stats, int64_t items) {
+  using S = typename T::S;
+  using L = LdsTile<T, BN, DP>;
+  constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
+  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[L::SIZE], v1[L::SIZE];
+  const int lane = threadIdx.x % kWave, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
+  const TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
+  const float c = p.scale * kLog2e;
+
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t tile = item / p.heads;
+    const int head = (int)(item - tile * p.heads);
+    const Tile t = find_tile(p.offsets, p.batch, p.tokens, tile, BM);
+    if (t.row >= t.last) continue;
+    const int64_t row = t.row + wave * 32 + (lane & 31);
+    const bool there = row < t.last;
+    S *dq = (S *)p.dq.data + row * p.dq.token + head * p.dq.head;
+    if (t.sequence < 0) {
+      if (there && half == 0 && p.fill & 1)
+        for (int d = 0; d < p.dim; ++d) dq[d] = 0;
+      continue;
+    }
+    const KeyRange range = keys_of(p.offsets, p.kv_offsets, p.batch, p.kv_tokens, t);
+    const SeenKeys seen(p.causal, range.count, t.last, t.row, BM, wave, row, there);
+    const int64_t count = (seen.tile_any + BN - 1) / BN;
+    const int kv_head = head / p.group;
+    const S *kbase = (const S *)p.k.data + range.first * p.k.token + kv_head * p.k.head;
+    const S *vbase = (const S *)p.v.data + range.first * p.v.token + kv_head * p.v.head;
+
+    Operand<T> q[STEPS], g[STEPS];
+    float delta = 0.0f;
+    {
+      const S *qat = (const S *)p.q.data + row * p.q.token + head * p.q.head;
+      const S *gat = (const S *)p.grad.data + row * p.grad.token + head * p.grad.head;
+      const S *oat = (const S *)p.out.data + row * p.out.token + head * p.out.head;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int at = s * 16 + half * 8;
+        q[s] = load_operand<T>(qat, at, p.dim, there);
+        g[s] = load_operand<T>(gat, at, p.dim, there);
+        delta = dot<T>(g[s], load_operand<T>(oat, at, p.dim, there), delta);
+      }
+    }
+    delta += __uint_as_float(lane_xor<32>(__float_as_uint(delta)));
+    float lse2 = there ? p.lse[row * p.heads + head] * kLog2e : INFINITY;
+    if (lse2 == -INFINITY) lse2 = INFINITY;
+    if (there && half == 0) stats[(int64_t)head * p.tokens + row] = RowStats{lse2, delta};
+
+    f32x16_t o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
+    auto fill = [&](u32x4_t *k, u32x4_t *v, int64_t n) {
+      kload.fill(k, kbase + n * BN * p.k.token, range.count - n * BN, p.k.token, p.dim, wave);
+      vload.fill(v, vbase + n * BN * p.v.token, range.count - n * BN, p.v.token, p.dim, wave);
+    };
+    auto work = [&](const u32x4_t *k, const u32x4_t *v, int64_t n) {
+      const int64_t base = n * BN;
+      if (base >= seen.wave_any) return;
+      const bool masked = base + BN > seen.wave_all;
+      const int left = (int)(seen.mine - base < BN ? seen.mine - base : BN);
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+        for (int e = 0; e < STEPS; ++e) {
+          s = multiply(read_rows<T, BN, DP>(k, j * 32, e, lane), q[e], s);
+          dp = multiply(read_rows<T, BN, DP>(v, j * 32, e, lane), g[e], dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (j * 32 + row_of(i, half) >= left) s[i] = 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const Operand<T> w = operand_of<T>(s, h);
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] = multiply(read_columns<T, BN, DP>(k, j * 32 + h * 16, d * 32, lane), w, o[d]);
+        }
+      }
+    };
+    if (count > 0) fill(k0, v0, 0);
+    for (int64_t n = 0; n < count; n += 2) {
+      landed();
+      if (n + 1 < count) fill(k1, v1, n + 1);
+      work(k0, v0, n);
+      if (n + 1 < count) {
+        landed();
+        if (n + 2 < count) fill(k0, v0, n + 2);
+        work(k1, v1, n + 1);
+      }
+    }
+    landed();
+    if (there) store_rows<T, DT>(dq, o, p.scale, half, p.dim);
+  }
+}
+
+// The statistics of a tile's rows, 32 a load; behind the last row zeros (whose
+// gradient is zero, too, so they add nothing).
+template <int BN, int WAVES>
+__device__ __forceinline__ void fill_stats(float *lds, const RowStats *stats, int64_t rows,
+                                           int wave, int lane) {
+  const int n = rows < BN ? (int)rows : BN;
+  const auto b = buffer_of(stats, (uint32_t)(n * sizeof(RowStats)));
+  for (int j = wave; j < BN / 32; j += WAVES)
+    load_to_lds(b, (j * kWave + lane) * 4, lds + j * kWave);
+}
+
+// Keys: dk and dv.  A lane holds one key of its wave's 32.
+template <typename T, int DP, int WAVES, int BN>
+__global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradParams p,
+                                                                 const RowStats *stats,
+                                                                 int kv_heads, int64_t items) {
+  using S = typename T::S;
+  using L = LdsTile<T, BN, DP>;
+  constexpr int BM = WAVES * 32, QT = BN / 32, STEPS = DP / 16, DT = DP / 32;
+  __shared__ u32x4_t q0[L::SIZE], g0[L::SIZE], q1[L::SIZE], g1[L::SIZE];
+  __shared__ float s0[BN * 2], s1[BN * 2];
+  const int lane = threadIdx.x % kWave, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
+  const TileLoad<T, BN, DP, WAVES> gload(wave, lane, p.grad.token, p.dim);
+  const float c = p.scale * kLog2e;
+  const int32_t *key_offsets = p.kv_offsets ? p.kv_offsets : p.offsets;
+
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t tile = item / kv_heads;
+    const int kv_head = (int)(item - tile * kv_heads);
+    const Tile t = find_tile(key_offsets, p.batch, p.kv_tokens, tile, BM);
+    if (t.row >= t.last) continue;
+    const int64_t key = t.row + wave * 32 + (lane & 31);
+    const bool there = key < t.last;
+    S *dk = (S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head;
+    S *dv = (S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head;
+    if (t.sequence < 0) {
+      if (there && half == 0) {
+        for (int d = 0; d < p.dim; ++d) {
+          if (p.fill & 2) dk[d] = 0;
+          if (p.fill & 4) dv[d] = 0;
+        }
+      }
+      continue;
+    }
+    int64_t first = t.first, rows = t.last - t.first;
+    if (p.kv_offsets) {
+      first = segment_start(p.offsets, p.batch, p.tokens, t.sequence + 1);
+      rows = segment_start(p.offsets, p.batch, p.tokens, t.sequence + 2) - first;
+      if (rows < 0) rows = 0;
+    }
+    // the first row that sees a key: as far from the last row as the key from
+    // the last key
+    auto first_row = [&](int64_t at) {
+      const int64_t r = p.causal ? rows - (t.last - at) : 0;
+      return r < 0 ? 0 : r;
+    };
+    const int64_t wave_key = t.row + wave * 32;
+    const int64_t wave_end = wave_key + 31 < t.last - 1 ? wave_key + 31 : t.last - 1;
+    // (a wave without keys has nothing to see)
+    const int64_t wave_from = wave_key < t.last ? first_row(wave_key) : rows;
+    const int64_t wave_full = wave_key < t.last ? first_row(wave_end) : rows;
+    const int64_t mine = there ? first_row(key) : rows;
+    const int64_t n0 = first_row(t.row) / BN;
+    const int64_t per_head = (rows + BN - 1) / BN - n0;
+    const int64_t count = per_head > 0 ? per_head * p.group : 0;
+
+    Operand<T> k[STEPS], v[STEPS];
+    {
+      const S *kat = (const S *)p.k.data + key * p.k.token + kv_head * p.k.head;
+      const S *vat = (const S *)p.v.data + key * p.v.token + kv_head * p.v.head;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        k[s] = load_operand<T>(kat, s * 16 + half * 8, p.dim, there);
+        v[s] = load_operand<T>(vat, s * 16 + half * 8, p.dim, there);
+      }
+    }
+    f32x16_t ok[DT], ov[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) ok[d] = ov[d] = f32x16_t{};
+
+    auto fill = [&](u32x4_t *q, u32x4_t *g, float *st, int64_t it) {
+      const int64_t h = it / per_head, n = n0 + it - h * per_head;
+      const int64_t head = kv_head * (int64_t)p.group + h, row = first + n * BN;
+      const int64_t left = rows - n * BN;
+      qload.fill(q, (const S *)p.q.data + row * p.q.token + head * p.q.head, left, p.q.token,
+                 p.dim, wave);
+      gload.fill(g, (const S *)p.grad.data + row * p.grad.token + head * p.grad.head, left,
+                 p.grad.token, p.dim, wave);
+      fill_stats<BN, WAVES>(st, stats + head * p.tokens + row, left, wave, lane);
+    };
+    auto work = [&](const u32x4_t *q, const u32x4_t *g, const float *st, int64_t it) {
+      const int64_t n = n0 + it % per_head, base = n * BN;
+      if (base + BN <= wave_from) return;
+      const bool masked = base < wave_full;
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+        for (int e = 0; e < STEPS; ++e) {
+          s = multiply(read_rows<T, BN, DP>(q, j * 32, e, lane), k[e], s);
+          dp = multiply(read_rows<T, BN, DP>(g, j * 32, e, lane), v[e], dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const f32x4_t *at =
+              reinterpret_cast<const f32x4_t *>(st + 2 * (j * 32 + row_of(i, half)));
+          const f32x4_t a = at[0], b = at[1];
+          const float lse2[4] = {a[0], a[2], b[0], b[2]}, delta[4] = {a[1], a[3], b[1], b[3]};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -lse2[e]));
+            dp[i + e] = s[i + e] * (dp[i + e] - delta[e]);
+          }
+        }
+        if (masked) {
+          const int from = mine - base < BN ? (int)(mine - base) : BN;   // rows of the tile before it do not see the key
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (j * 32 + row_of(i, half) < from) s[i] = dp[i] = 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const Operand<T> wp = operand_of<T>(s, h), wd = operand_of<T>(dp, h);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            ov[d] = multiply(read_columns<T, BN, DP>(g, j * 32 + h * 16, d * 32, lane), wp, ov[d]);
+            ok[d] = multiply(read_columns<T, BN, DP>(q, j * 32 + h * 16, d * 32, lane), wd, ok[d]);
+          }
+        }
+      }
+    };
+    if (count > 0) fill(q0, g0, s0, 0);
+    for (int64_t n = 0; n < count; n += 2) {
+      landed();
+      if (n + 1 < count) fill(q1, g1, s1, n + 1);
+      work(q0, g0, s0, n);
+      if (n + 1 < count) {
+        landed();
+        if (n + 2 < count) fill(q0, g0, s0, n + 2);
+        work(q1, g1, s1, n + 1);
+      }
+    }
+    landed();
+    if (there) {
+      store_rows<T, DT>(dk, ok, p.scale, half, p.dim);
+      store_rows<T, DT>(dv, ov, 1.0f, half, p.dim);
+    }
+  }
+}
+
+template <typename T, int DP, int WAVES, int BN>
+hipError_t run(const AttentionGradParams &p, RowStats *stats, hipStream_t stream) {
+  const dim3 block(WAVES * kWave);
+  if (p.tokens) {
+    const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
+    launch_kernel(grad_rows_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), block, 0, stream, p,
+                  stats, items);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!p.kv_tokens) return hipSuccess;
+  const int kv_heads = p.heads / p.group;
+  const int64_t items = tile_count(p.kv_tokens, p.batch, WAVES * 32) * kv_heads;
+  launch_kernel(grad_keys_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), block, 0, stream, p,
+                (const RowStats *)stats, kv_heads, items);
+  return hipGetLastError();
+}
+
+template <typename T, int WAVES, int BN>
+hipError_t by_dim(const AttentionGradParams &p, RowStats *stats, hipStream_t stream) {
+  if (p.dim <= 32) return run<T, 32, WAVES, BN>(p, stats, stream);
+  if (p.dim <= 64) return run<T, 64, WAVES, BN>(p, stats, stream);
+  if (p.dim <= 96) return run<T, 96, WAVES, BN>(p, stats, stream);
+  return run<T, 128, WAVES, BN>(p, stats, stream);
+}
+
+}  // namespace
+
+size_t attention_grad_workspace(int64_t tokens, int heads) {
+  return (size_t)tokens * heads * sizeof(RowStats);
+}
+
+hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *ws,
+                                 hipStream_t stream) {
+  RowStats *stats = (RowStats *)ws;
+  const bool few = (p.tokens > p.kv_tokens ? p.tokens : p.kv_tokens) / p.batch <= 48;
+  if (dtype == kF32)
+    return few ? by_dim<F32, 1, 32>(p, stats, stream) : by_dim<F32, 4, 32>(p, stats, stream);
+  return few ? by_dim<BF16, 1, 32>(p, stats, stream) : by_dim<BF16, 4, 64>(p, stats, stream);
+}
+
+}  // namespace dlrm

@@ -20,14 +20,6 @@
 namespace dlrm {
 namespace {
 
-// LDS operations and loads to LDS of this wave have landed, and everyone's.
-__device__ __forceinline__ void landed() {
-  __builtin_amdgcn_s_waitcnt(0x0070);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Masks of the elements of a word that are not finite.
 template <typename T>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -111,28 +103,12 @@ __global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams
       if (there && half == 0 && p.fill & 2) p.lse[row * p.heads + head] = -INFINITY;
       continue;
     }
-    int64_t kfirst = t.first, klast = t.last;
-    if (p.kv_offsets) {
-      kfirst = segment_start(p.kv_offsets, p.batch, p.kv_tokens, t.sequence + 1);
-      klast = segment_start(p.kv_offsets, p.batch, p.kv_tokens, t.sequence + 2);
-    }
-    const int64_t keys = klast > kfirst ? klast - kfirst : 0;
-    // keys that a row sees: all, or those up to its own place from the end
-    auto seen_by = [&](int64_t r) {
-      const int64_t n = p.causal ? keys - (t.last - 1 - r) : keys;
-      return n < 0 ? 0 : n;
-    };
-    const int64_t mine = there ? seen_by(row) : 0;
-    const int64_t wave_first = t.row + wave * 32;
-    const int64_t wave_last = wave_first + 31 < t.last - 1 ? wave_first + 31 : t.last - 1;
-    const int64_t wave_any = wave_first < t.last ? seen_by(wave_last) : 0;   // any row sees
-    const int64_t wave_all = wave_first + 31 < t.last ? seen_by(wave_first) : 0;  // all rows see
-    const int64_t tile_last = t.row + BM - 1 < t.last - 1 ? t.row + BM - 1 : t.last - 1;
-    const int64_t count = (seen_by(tile_last) + BN - 1) / BN;
-
+    const KeyRange range = keys_of(p.offsets, p.kv_offsets, p.batch, p.kv_tokens, t);
+    const SeenKeys seen(p.causal, range.count, t.last, t.row, BM, wave, row, there);
+    const int64_t count = (seen.tile_any + BN - 1) / BN;
     const int kv_head = head / p.group;
-    const S *kbase = (const S *)p.k.data + kfirst * p.k.token + kv_head * p.k.head;
-    const S *vbase = (const S *)p.v.data + kfirst * p.v.token + kv_head * p.v.head;
+    const S *kbase = (const S *)p.k.data + range.first * p.k.token + kv_head * p.k.head;
+    const S *vbase = (const S *)p.v.data + range.first * p.v.token + kv_head * p.v.head;
     Operand<T> q[STEPS];
     {
       const S *at = (const S *)p.q.data + row * p.q.token + head * p.q.head;
@@ -146,13 +122,13 @@ __global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams
     float m = -INFINITY, l = 0.0f;
 
     auto fill = [&](u32x4_t *k, u32x4_t *v, int64_t n) {
-      kload.fill(k, kbase + n * BN * p.k.token, keys - n * BN, p.k.token, p.dim, wave);
-      vload.fill(v, vbase + n * BN * p.v.token, keys - n * BN, p.v.token, p.dim, wave);
+      kload.fill(k, kbase + n * BN * p.k.token, range.count - n * BN, p.k.token, p.dim, wave);
+      vload.fill(v, vbase + n * BN * p.v.token, range.count - n * BN, p.v.token, p.dim, wave);
     };
     auto work = [&](const u32x4_t *k, const u32x4_t *v, int64_t n) {
       const int64_t base = n * BN;
-      if (base >= wave_any) return;
-      const bool masked = base + BN > wave_all;
+      if (base >= seen.wave_any) return;
+      const bool masked = base + BN > seen.wave_all;
       f32x16_t s[KT];
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
@@ -162,7 +138,7 @@ __global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams
           s[j] = multiply(read_rows<T, BN, DP>(k, j * 32, e, lane), q[e], s[j]);
       }
       if (masked) {
-        const int left = (int)(mine - base < BN ? mine - base : BN);
+        const int left = (int)(seen.mine - base < BN ? seen.mine - base : BN);
 #pragma unroll
         for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -204,7 +180,7 @@ __global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams
             bad |= any_not_finite<T>(read_columns<T, BN, DP>(v, j * 16, d * 32, lane));
       }
       if (__any(bad)) {
-        const int left = (int)(mine - base < BN ? mine - base : BN);
+        const int left = (int)(seen.mine - base < BN ? seen.mine - base : BN);
 #pragma unroll
         for (int j = 0; j < BN / 16; ++j) {
           const Operand<T> w = operand_of<T>(s[j >> 1], j & 1);
@@ -279,8 +255,7 @@ __global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams
 template <typename T, int DP, int WAVES, int BN>
 hipError_t run(const AttentionParams &p, hipStream_t stream) {
   const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
-  const int64_t grid = items < (1 << 22) ? items : 1 << 22;
-  launch_kernel(attention_kernel<T, DP, WAVES, BN>, dim3((uint32_t)grid), dim3(WAVES * kWave), 0,
+  launch_kernel(attention_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), dim3(WAVES * kWave), 0,
                 stream, p, items);
   return hipGetLastError();
 }

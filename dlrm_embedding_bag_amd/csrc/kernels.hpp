@@ -324,4 +324,19 @@ struct AttentionParams {
 };
 hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream);
 
+struct AttentionGradParams {
+  int64_t tokens, kv_tokens, batch;
+  int heads, group, dim;
+  HeadRows grad, q, k, v, out;  // grad: of out
+  const float *lse;             // (tokens, heads)
+  const int32_t *offsets, *kv_offsets;
+  int causal;
+  float scale;
+  int fill;  // 1: zeros in dq, 2: in dk, 4: in dv, for rows outside all sequences
+  HeadRowsOut dq, dk, dv;
+};
+size_t attention_grad_workspace(int64_t tokens, int heads);
+hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *ws,
+                                 hipStream_t stream);
+
 }  // namespace dlrm

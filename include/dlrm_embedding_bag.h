@@ -775,6 +775,39 @@ DLRM_API int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, 
                               float scale, int32_t fill, void *out, int64_t o_token,
                               int64_t o_head, float *lse, void *stream);
 
+/*
+ * attention_packed_grad -- the gradients of attention_packed's out with respect
+ * to q, k and v, from its inputs and outputs.  Over the keys that a row sees,
+ *   p  = exp(scale * q . k - lse)
+ *   ds = p * (grad . v - grad . out)
+ *   dq = scale * sum ds k     dk = scale * sum ds q     dv = sum p grad
+ * dk and dv are summed over the heads that share a key head.  Sums are in float32
+ * in a fixed order; for bfloat16 p and ds are rounded to bfloat16 before the last
+ * products; the results are rounded once.  A row whose lse is -inf has dq 0 and
+ * adds nothing.  A NaN or an infinity may reach all gradients of its sequence,
+ * but none of another.
+ *
+ *   grad, out   as out in attention_packed; lse (tokens, heads) as it wrote it
+ *   q, grad     token strides up to 2^22 elements, as those of k and v
+ *   fill        rows outside all sequences: 0 they are left as they are; + 1
+ *               they are zero in dq, + 2 in dk, + 4 in dv
+ *   dq, dk, dv  as q, k, v; they must not overlap the inputs
+ *   workspace   16-byte aligned, at least attention_packed_grad_workspace_bytes(
+ *               tokens, heads) bytes (0 for sizes that the call refuses, and
+ *               without tokens, where it may be NULL); it needs no clearing
+ *   The rest as for attention_packed.
+ */
+DLRM_API size_t attention_packed_grad_workspace_bytes(int64_t tokens, int32_t heads);
+DLRM_API int attention_packed_grad(
+    int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t heads, int32_t kv_heads, int32_t dim,
+    int32_t dtype, const void *grad, int64_t g_token, int64_t g_head, const void *q,
+    int64_t q_token, int64_t q_head, const void *k, int64_t k_token, int64_t k_head, const void *v,
+    int64_t v_token, int64_t v_head, const void *out, int64_t o_token, int64_t o_head,
+    const float *lse, const int32_t *offsets, const int32_t *kv_offsets, int32_t causal,
+    float scale, int32_t fill, void *dq, int64_t dq_token, int64_t dq_head, void *dk,
+    int64_t dk_token, int64_t dk_head, void *dv, int64_t dv_token, int64_t dv_head,
+    void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

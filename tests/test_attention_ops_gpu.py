@@ -394,3 +394,173 @@ def test_attention_bad_offsets_stay_within_the_tensors():
         out, _ = fw.attention_packed(q, q, q, off, off.flip(0).contiguous())
         assert out.shape == q.shape
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------- gradient of packed attention --
+def _gradient_want(grad, q, k, v, out, lse, off, koff, causal, scale, kind):
+    """dq, dk, dv from the formula with the given out and lse, and their tolerances."""
+    grad, q, k, v, out, lse = (_np64(t) for t in (grad, q, k, v, out, lse))
+    off = off.numpy()
+    koff = off if koff is None else koff.numpy()
+    heads, dim = q.shape[1:]
+    group = heads // k.shape[1]
+    want = [np.zeros(t.shape) for t in (q, k, v)]
+    tol = [np.zeros(t.shape) for t in (q, k, v)]
+    ub = U["bf16"] if kind == "bf16" else 0.0
+    for b in range(len(off) - 1):
+        qs, ks = slice(off[b], off[b + 1]), slice(koff[b], koff[b + 1])
+        nq, nk = off[b + 1] - off[b], koff[b + 1] - koff[b]
+        if nq == 0 or nk == 0:
+            continue
+        seen = _seen(nq, nk, causal)
+        for h in range(heads):
+            g = h // group
+            Q, K, V, G, O = q[qs, h], k[ks, g], v[ks, g], grad[qs, h], out[qs, h]
+            s = Q @ K.T * scale
+            size = np.abs(Q) @ np.abs(K).T * scale
+            l = np.where(np.isinf(lse[qs, h]), 0.0, lse[qs, h])[:, None]
+            p = np.where(seen, np.exp(np.where(seen, s - l, 0.0)), 0.0)
+            e = (dim * size + 4 * np.abs(s) + 4 * np.abs(l) + 4) * U32     # relative, of p
+            inner = G @ V.T - (G * O).sum(1, keepdims=True)
+            # both inner products, their difference and the product with p
+            off_inner = (dim + 2) * U32 * (np.abs(G) @ np.abs(V).T
+                                           + (np.abs(G) * np.abs(O)).sum(1, keepdims=True))
+            ds = p * inner
+            dtol = p * off_inner + (e + ub + 2 * U32) * np.abs(ds)
+            ptol = (e + ub) * p
+            terms = (nq * group + nk + 8) * U32
+            want[0][qs, h] += scale * ds @ K
+            tol[0][qs, h] += scale * (dtol + terms * np.abs(ds)) @ np.abs(K)
+            want[1][ks, g] += scale * ds.T @ Q
+            tol[1][ks, g] += scale * (dtol + terms * np.abs(ds)).T @ np.abs(Q)
+            want[2][ks, g] += p.T @ G
+            tol[2][ks, g] += (ptol + terms * p).T @ np.abs(G)
+    return want, [t + U[kind] * np.abs(w) + TINY for t, w in zip(tol, want)]
+
+
+def _packed_inputs(lengths, past, heads, kv, dim, kind, seed=0):
+    off, koff = _sequences(lengths, past)
+    n, m = int(off[-1]), int(off[-1] if koff is None else koff[-1])
+    g = _gen(n + dim + seed)
+    q = _randn(g, n, heads, dim, scale=1.5).to(_dt(kind))
+    k, v = (_randn(g, m, kv, dim).to(_dt(kind)) for _ in range(2))
+    return off, koff, q, k, v, _randn(g, n, heads, dim).to(_dt(kind))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths,past,heads,kv,dim,causal", PACKED)
+def test_attention_gradient(lengths, past, heads, kv, dim, causal, kind):
+    import dlrm_embedding_bag_amd as fw
+    off, koff, q, k, v, grad = _packed_inputs(lengths, past, heads, kv, dim, kind)
+    scale = None if dim % 16 else 0.3
+    cuda = [None if t is None else t.cuda() for t in (off, koff)]
+    out, lse = fw.attention_packed(q.cuda(), k.cuda(), v.cuda(), *cuda, causal=causal, scale=scale)
+    want, tol = _gradient_want(grad, q, k, v, out, lse, off, koff, causal,
+                               dim ** -0.5 if scale is None else scale, kind)
+    layout = ("plain", "slice", "heads")[(len(q) + dim // 8) % 3]
+    first = None
+    for layout in ("plain", layout):
+        got = fw.attention_packed_grad(_laid(grad, layout), _laid(q, layout), _laid(k, layout),
+                                       _laid(v, layout), _laid(out.cpu(), layout), lse, *cuda,
+                                       causal=causal, scale=scale)
+        for a, w, t, what in zip(got, want, tol, "qkv"):
+            _assert_within(_np64(a), w, t, what)
+        if first is None:
+            first = got
+        for a, b in zip(first, got):      # the same sums in the same order
+            assert bool((a == b).all())
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_gradient_against_differences(causal):
+    """Of sum(out * grad), along random directions, by central differences in 64
+    bits of the definition on the host."""
+    import dlrm_embedding_bag_amd as fw
+    off, koff, q, k, v, grad = _packed_inputs([9, 20, 1], [3, 0, 7], 4, 2, 24, "f32", 5)
+    scale = 24 ** -0.5
+    out, lse = fw.attention_packed(q.cuda(), k.cuda(), v.cuda(), off.cuda(), koff.cuda(),
+                                   causal=causal)
+    got = fw.attention_packed_grad(grad.cuda(), q.cuda(), k.cuda(), v.cuda(), out, lse, off.cuda(),
+                                   koff.cuda(), causal=causal)
+    base = [_np64(t) for t in (q, k, v)]
+    rng = np.random.default_rng(0)
+    import torch
+    for i in range(3):
+        d = rng.standard_normal(base[i].shape)
+        h = 1e-5
+        value = []
+        for sign in (1, -1):
+            at = [torch.from_numpy(b + sign * h * d if j == i else b) for j, b in enumerate(base)]
+            o = _attention_want(*at, off, koff, causal, scale, "f32")[0]
+            value.append((o * _np64(grad)).sum())
+        want = (value[0] - value[1]) / (2 * h)
+        # third derivatives times h^2 / 6 stay below 1e-7 here; float32 sums of
+        # some 3000 terms of about 1 leave 3000 u32 of their square root's size
+        assert abs((_np64(got[i]) * d).sum() - want) <= 1e-3 + 1e-5 * abs(want)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[5, 9], [100, 200, 40]])
+def test_attention_gradient_outside_the_sequences(lengths, kind):
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    n, lead, tail = sum(lengths), 3, 200
+    off = torch.tensor(lead + np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32).cuda()
+    _, _, q, k, v, grad = (None if t is None else t.cuda()
+                           for t in _packed_inputs(lengths, None, 4, 2, 64, kind))
+    out, lse = fw.attention_packed(q, k, v, off - lead)
+    want = fw.attention_packed_grad(grad, q, k, v, out, lse, off - lead)
+
+    def wide(t):
+        buf = torch.full((n + lead + tail, *t.shape[1:]), float("nan"), dtype=t.dtype,
+                         device="cuda")
+        buf[lead:lead + n] = t
+        return buf
+
+    args = [wide(t) for t in (grad, q, k, v, out, lse)]
+    got = fw.attention_packed_grad(*args, off)
+    given = [torch.full_like(t, 7.0) for t in got]
+    ws = torch.empty(fw.attention_packed_grad_workspace_bytes(n + lead + tail, 4),
+                     dtype=torch.uint8, device="cuda")
+    back = fw.attention_packed_grad(*args, off, out_q=given[0], out_k=given[1], out_v=given[2],
+                                    workspace=ws)
+    for a, b, c, w in zip(got, given, back, want):
+        assert c is b and torch.equal(a[lead:lead + n], w) and torch.equal(b[lead:lead + n], w)
+        for part in (slice(0, lead), slice(lead + n, None)):
+            assert not a[part].any() and (b[part] == 7.0).all()
+
+
+def test_attention_gradient_stays_within_its_sequence():
+    """A sequence with values that are not finite leaves the others' gradients."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, v, grad = _packed_inputs([40, 70, 33], None, 4, 2, 64, "f32")
+    off, q, k, v, grad = (t.cuda() for t in (off, q, k, v, grad))
+    out, lse = fw.attention_packed(q, k, v, off)
+    want = fw.attention_packed_grad(grad, q, k, v, out, lse, off)
+    grad[50, 1, 3] = math.nan
+    v[60, 0, 1] = math.inf
+    k[70, 1, 1] = math.nan
+    out, lse = fw.attention_packed(q, k, v, off)
+    got = fw.attention_packed_grad(grad, q, k, v, out, lse, off)
+    for a, w in zip(got, want):
+        assert torch.equal(a[:40], w[:40]) and torch.equal(a[110:], w[110:])
+
+
+def test_attention_gradient_without_queries_or_keys():
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    q = torch.randn(6, 2, 32, device="cuda")
+    none = q[:0]
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    out, lse = fw.attention_packed(q, none, none, off, zero)
+    assert not out.any() and (lse == -math.inf).all()
+    dq, dk, dv = fw.attention_packed_grad(q, q, none, none, out, lse, off, zero)
+    assert not dq.any() and dk.shape == dv.shape == (0, 2, 32)
+    out, lse = fw.attention_packed(none, q, q, zero, off)
+    dq, dk, dv = fw.attention_packed_grad(none, none, q, q, out, lse, zero, off)
+    assert dq.shape == (0, 2, 32) and not dk.any() and not dv.any()

@@ -11,7 +11,9 @@ from .abi import (  # noqa: F401
     dlrm_forward_workspace_bytes, dlrm_interact_lower_tri, emb_bag_pool, emb_bag_sum_multi,
     linear_bias_act, linear_bias_act_split, load, mlp_forward)
 from .attention_ops import (  # noqa: F401
-    attention_packed, attention_packed_grad, attention_packed_grad_workspace_bytes, qk_norm_rope, qk_norm_rope_grad, qk_norm_rope_grad_workspace_bytes)
+    KVCache, attention_cached, attention_cached_workspace_bytes, attention_packed,
+    attention_packed_grad, attention_packed_grad_workspace_bytes, kv_cache, kv_cache_read,
+    kv_cache_write, qk_norm_rope, qk_norm_rope_grad, qk_norm_rope_grad_workspace_bytes)
 from .token_ops import (  # noqa: F401
     emb_lookup_grad, emb_lookup_grad_workspace_bytes, emb_lookup_scaled, linear_i8_bias_act,
     rms_norm_residual_i8)

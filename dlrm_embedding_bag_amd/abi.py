@@ -38,7 +38,9 @@ EXPORTS = ("dlrm_status_string", "dlrm_abi_version", "dlrm_set_kernel_timing_eve
            "emb_lookup_scaled", "emb_lookup_grad_workspace_bytes", "emb_lookup_grad",
            "rms_norm_residual_i8", "linear_i8_bias_act",
            "qk_norm_rope", "qk_norm_rope_grad_workspace_bytes", "qk_norm_rope_grad",
-           "attention_packed", "attention_packed_grad_workspace_bytes", "attention_packed_grad")
+           "attention_packed", "attention_packed_grad_workspace_bytes", "attention_packed_grad",
+           "kv_cache_write", "kv_cache_read", "attention_cached_workspace_bytes",
+           "attention_cached")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -172,6 +174,16 @@ def load(path: str = LIB_PATH):
     lib.attention_packed_grad.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32, _i32, *rows, *rows,
                                           *rows, *rows, *rows, _vp, _vp, _vp, _i32, f32, _i32,
                                           *rows, *rows, *rows, _vp, size, _vp]
+    cache = [_i64, _i32, _i32, _vp, _vp, _vp, _vp]  # pages, page, bits, codes and scales
+    lib.kv_cache_write.restype = ctypes.c_int
+    lib.kv_cache_write.argtypes = [_i64, _i32, _i32, _i32, *rows, *rows, _vp, *cache, _vp]
+    lib.kv_cache_read.restype = ctypes.c_int
+    lib.kv_cache_read.argtypes = [_i64, _i32, _i32, _i32, _vp, *cache, *rows, *rows, _vp]
+    lib.attention_cached_workspace_bytes.restype = size
+    lib.attention_cached_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i32]
+    lib.attention_cached.restype = ctypes.c_int
+    lib.attention_cached.argtypes = [_i64, _i32, _i32, _i32, _i32, *rows, *cache, _vp, _i64, _i64,
+                                     _vp, f32, *rows, _vp, size, _vp]
     if path == LIB_PATH:
         _LIB = lib
     return lib

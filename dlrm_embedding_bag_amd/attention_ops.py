@@ -1,5 +1,6 @@
-"""Attention operators: norm and rotation of query and key heads, and attention
-over packed sequences, with their gradients.
+"""Attention operators: norm and rotation of query and key heads and attention
+over packed sequences, with their gradients; a paged cache of keys and values in
+8 or 4 bits, and attention of single tokens over it.
 
 Argument marshalling only, as in token_ops.py: every function has the name of
 the C entry point it calls (include/dlrm_embedding_bag.h says what it computes),
@@ -13,6 +14,8 @@ contiguous; tokens and heads may have any stride, so slices of a joint product
 and transposed views go in as they are.
 """
 from __future__ import annotations
+
+from typing import Any, NamedTuple
 
 from .abi import _check, load
 from .token_ops import _CODES, _INT_MAX, _device, _handle, _on, _torch, _vector
@@ -296,3 +299,146 @@ def attention_packed_grad(grad, q, k, v, out, lse, offsets, kv_offsets=None, cau
         _check(status, "attention_packed_grad")
     _mark(torch, given)
     return out_q, out_k, out_v
+
+
+class KVCache(NamedTuple):
+    """A paged cache's uint8 tensors: codes (pages, heads, page, dim * bits / 8)
+    and scales (pages, heads, page, dim / 32) of keys and of values."""
+    k_codes: Any
+    k_scales: Any
+    v_codes: Any
+    v_scales: Any
+
+
+def kv_cache(pages, page, heads, dim, bits=8, device=None):
+    """A new KVCache of `pages` pages of `page` rows on `device` (the current
+    GPU), all of it zeros."""
+    torch = _torch()
+    if bits not in (4, 8) or dim not in (32, 64, 128):
+        raise ValueError("bits must be 4 or 8, and dim 32, 64 or 128")
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return KVCache(*(torch.zeros((pages, heads, page, n), dtype=torch.uint8, device=device)
+                     for n in (dim * bits // 8, dim // 32) * 2))
+
+
+def _cache(torch, cache, dev):
+    """pages, page, bits and pointers of a cache, its heads and dim."""
+    codes, scales = cache[0], cache[1]
+    for i, t in enumerate(cache):
+        what = KVCache._fields[i]
+        _on(torch, t, what, dev)
+        if t.dtype is not torch.uint8:
+            raise TypeError(f"{what} must be torch.uint8 (got {t.dtype})")
+        if t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous (pages, heads, page, bytes)")
+    if codes.shape != cache[2].shape or scales.shape != cache[3].shape or (
+            codes.shape[:3] != scales.shape[:3]):
+        raise ValueError("codes and scales of keys and values must have the same pages, heads, "
+                         "page and dim")
+    pages, heads, page, row = codes.shape
+    dim = scales.shape[3] * 32
+    if not dim or row * 8 % dim or row * 8 // dim not in (4, 8):
+        raise ValueError("codes must have 32 or 16 bytes for each byte of the scales")
+    if pages > _INT_MAX or heads > _INT_MAX or page > _INT_MAX or dim > _INT_MAX:
+        raise ValueError(f"the cache has a dimension above {_INT_MAX}")
+    return (pages, page, row * 8 // dim, codes.data_ptr(), scales.data_ptr(), cache[2].data_ptr(),
+            cache[3].data_ptr()), heads, dim
+
+
+def kv_cache_write(cache, k, v, slots, stream=None):
+    """Token t's keys and values, (tokens, heads, dim) float32 or bfloat16, into
+    row slots[t] of the cache, int32: row slot % page of page slot // page.
+    Tokens whose slot is outside the cache are not written."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_of(torch, k, "k")
+    dev = _device(torch, k, "k")
+    n, heads, dim, kt, kh = _heads(torch, k, "k", dtype, dev)
+    vn, vh, vd, vt, vhs = _heads(torch, v, "v", dtype, dev)
+    places, cheads, cdim = _cache(torch, cache, dev)
+    if (vn, vh, vd) != (n, heads, dim) or (cheads, cdim) != (heads, dim):
+        raise ValueError("k and v must have the same shape, and the cache's heads and dim")
+    status = lib.kv_cache_write(n, heads, dim, _CODES[dtype], k.data_ptr(), kt, kh, v.data_ptr(),
+                                vt, vhs, _ints(torch, slots, "slots", n, dev), *places,
+                                _handle(torch, stream, dev))
+    if status:
+        _check(status, "kv_cache_write")
+    _mark(torch, cache)
+
+
+def kv_cache_read(cache, slots, out_dtype=None, out_k=None, out_v=None, stream=None):
+    """(k, v): the values that the cache's rows slots[t] stand for, as (tokens,
+    heads, dim) of out_dtype (bfloat16 unless given; float32); zeros for a slot
+    outside the cache."""
+    torch = _torch()
+    lib = load()
+    dev = _device(torch, cache[0], "k_codes")
+    places, heads, dim = _cache(torch, cache, dev)
+    pos = _ints(torch, slots, "slots", None, dev)
+    n = slots.numel()
+    given = (out_k, out_v)
+    for t in given:
+        if t is not None and out_dtype is None:
+            out_dtype = _dtype_of(torch, t, "out_k or out_v")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16 (got {out_dtype})")
+    out_k, kt, kh = _rows_out(torch, out_k, "out_k", (n, heads, dim), cache[0], stream, out_dtype,
+                              dev)
+    out_v, vt, vh = _rows_out(torch, out_v, "out_v", (n, heads, dim), cache[0], stream, out_dtype,
+                              dev)
+    status = lib.kv_cache_read(n, heads, dim, _CODES[out_dtype], pos, *places, out_k.data_ptr(), kt,
+                               kh, out_v.data_ptr(), vt, vh, _handle(torch, stream, dev))
+    if status:
+        _check(status, "kv_cache_read")
+    _mark(torch, given)
+    return out_k, out_v
+
+
+def attention_cached_workspace_bytes(batch, heads, kv_heads, dim, max_pages, page):
+    """Bytes of workspace that attention_cached takes for these sizes."""
+    return load().attention_cached_workspace_bytes(batch, min(heads, _INT_MAX),
+                                                   min(kv_heads, _INT_MAX), min(dim, _INT_MAX),
+                                                   max_pages, min(page, _INT_MAX))
+
+
+def attention_cached(q, cache, table, lengths, scale=None, out=None, workspace=None, stream=None):
+    """Attention of one query for each sequence, q (batch, heads, dim), over its
+    first lengths[b] keys and values in the cache: key j lies in row j % page of
+    page table[b, j // page].  table is int32 (batch, max_pages), lengths int32
+    (batch,); heads of q share those of the cache in equal groups.  `scale` is
+    dim ** -0.5 unless given.  `workspace` is a uint8 tensor of at least
+    attention_cached_workspace_bytes; without it one is allocated for the call."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_of(torch, q, "q")
+    dev = _device(torch, q, "q")
+    n, heads, dim, qt, qh = _heads(torch, q, "q", dtype, dev)
+    places, kv_heads, cdim = _cache(torch, cache, dev)
+    if cdim != dim:
+        raise ValueError("q must have the cache's dim")
+    _on(torch, table, "table", dev)
+    if table.dtype is not torch.int32:
+        raise TypeError(f"table must be torch.int32 (got {table.dtype})")
+    if table.dim() != 2 or table.shape[0] != n or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be (batch, max_pages) with unit column stride")
+    most = table.shape[1]
+    if most > _INT_MAX:
+        raise ValueError(f"table has more than {_INT_MAX} columns")
+    lp = _ints(torch, lengths, "lengths", n, dev)
+    if scale is None:
+        scale = dim ** -0.5
+    given = (out,)
+    out, ot, oh = _rows_out(torch, out, "out", (n, heads, dim), q, stream, dtype, dev)
+    size = lib.attention_cached_workspace_bytes(n, heads, kv_heads, dim, most, places[1])
+    ws, size, _hold = _scratch(torch, workspace, size, q, stream, dev)
+    status = lib.attention_cached(n, heads, kv_heads, dim, _CODES[dtype], q.data_ptr(), qt, qh,
+                                  *places, table.data_ptr(), table.stride(0) if n > 1 else most,
+                                  most, lp, scale, out.data_ptr(), ot, oh, ws, size,
+                                  _handle(torch, stream, dev))
+    if status:
+        _check(status, "attention_cached")
+    _mark(torch, given)
+    return out

@@ -57,6 +57,15 @@ int attention_shape(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t he
   return dim > DLRM_MAX_ATTENTION_DIM ? DLRM_ERR_UNSUPPORTED : DLRM_OK;
 }
 
+// DLRM_ERR_UNSUPPORTED only for what a cache could hold and this one does not.
+int cache_shape(int32_t heads, int32_t dim, int64_t pages, int32_t page, int32_t bits) {
+  if (heads < 1 || heads > kMaxHeads || pages < 1 || dim < 1 || page < 1) return DLRM_ERR_SHAPE;
+  if ((bits != 4 && bits != 8) || (dim != 32 && dim != 64 && dim != 128) || page < 16 ||
+      page > DLRM_MAX_CACHE_PAGE || (page & (page - 1)))
+    return DLRM_ERR_UNSUPPORTED;
+  return pages * (__int128)page > INT32_MAX ? DLRM_ERR_SHAPE : DLRM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -246,6 +255,126 @@ int attention_packed_grad(int64_t tokens, int64_t kv_tokens, int64_t batch, int3
   p.dk = {dk, dk_token, dk_head};
   p.dv = {dv, dv_token, dv_head};
   return status_of(launch_attention_grad(p, dtype, workspace, (hipStream_t)stream));
+}
+
+int kv_cache_write(int64_t tokens, int32_t heads, int32_t dim, int32_t dtype, const void *k,
+                   int64_t k_token, int64_t k_head, const void *v, int64_t v_token, int64_t v_head,
+                   const int32_t *slots, int64_t pages, int32_t page, int32_t bits, void *k_codes,
+                   void *k_scales, void *v_codes, void *v_scales, void *stream) {
+  if (tokens < 0 || tokens > INT32_MAX || !float_dtype(dtype)) return DLRM_ERR_SHAPE;
+  const int bad = cache_shape(heads, dim, pages, page, bits);
+  if (bad) return bad;
+  if (!in_rows(k_token, k_head) || !in_rows(v_token, v_head)) return DLRM_ERR_SHAPE;
+  if (tokens == 0) return DLRM_OK;
+  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales) return DLRM_ERR_NULL;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales))
+    return DLRM_ERR_UNSUPPORTED;
+  CacheParams p{};
+  p.tokens = tokens;
+  p.pages = pages;
+  p.heads = heads;
+  p.dim = dim;
+  p.page = page;
+  p.slots = slots;
+  p.k = k;
+  p.v = v;
+  p.k_token = k_token;
+  p.k_head = k_head;
+  p.v_token = v_token;
+  p.v_head = v_head;
+  p.k_codes = (uint8_t *)k_codes;
+  p.k_scales = (uint8_t *)k_scales;
+  p.v_codes = (uint8_t *)v_codes;
+  p.v_scales = (uint8_t *)v_scales;
+  return status_of(launch_cache_write(p, dtype, bits, (hipStream_t)stream));
+}
+
+int kv_cache_read(int64_t tokens, int32_t heads, int32_t dim, int32_t dtype, const int32_t *slots,
+                  int64_t pages, int32_t page, int32_t bits, const void *k_codes,
+                  const void *k_scales, const void *v_codes, const void *v_scales, void *k,
+                  int64_t k_token, int64_t k_head, void *v, int64_t v_token, int64_t v_head,
+                  void *stream) {
+  if (tokens < 0 || tokens > INT32_MAX || !float_dtype(dtype)) return DLRM_ERR_SHAPE;
+  const int bad = cache_shape(heads, dim, pages, page, bits);
+  if (bad) return bad;
+  if (!out_rows(tokens, heads, dim, k_token, k_head) ||
+      !out_rows(tokens, heads, dim, v_token, v_head))
+    return DLRM_ERR_SHAPE;
+  if (tokens == 0) return DLRM_OK;
+  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales) return DLRM_ERR_NULL;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales))
+    return DLRM_ERR_UNSUPPORTED;
+  CacheParams p{};
+  p.tokens = tokens;
+  p.pages = pages;
+  p.heads = heads;
+  p.dim = dim;
+  p.page = page;
+  p.slots = slots;
+  p.out_k = k;
+  p.out_v = v;
+  p.k_token = k_token;
+  p.k_head = k_head;
+  p.v_token = v_token;
+  p.v_head = v_head;
+  p.k_codes = (uint8_t *)const_cast<void *>(k_codes);
+  p.k_scales = (uint8_t *)const_cast<void *>(k_scales);
+  p.v_codes = (uint8_t *)const_cast<void *>(v_codes);
+  p.v_scales = (uint8_t *)const_cast<void *>(v_scales);
+  return status_of(launch_cache_read(p, dtype, bits, (hipStream_t)stream));
+}
+
+size_t attention_cached_workspace_bytes(int64_t batch, int32_t heads, int32_t kv_heads, int32_t dim,
+                                        int64_t max_pages, int32_t page) {
+  if (batch < 1 || batch > INT32_MAX || kv_heads < 1 || heads < kv_heads || heads > kMaxHeads ||
+      heads % kv_heads || max_pages < 0 || max_pages > INT32_MAX ||
+      cache_shape(kv_heads, dim, 1, page, 8))
+    return 0;
+  return cached_workspace(batch, heads, kv_heads, dim, max_pages, page);
+}
+
+int attention_cached(int64_t batch, int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype,
+                     const void *q, int64_t q_token, int64_t q_head, int64_t pages, int32_t page,
+                     int32_t bits, const void *k_codes, const void *k_scales, const void *v_codes,
+                     const void *v_scales, const int32_t *table, int64_t ld_table,
+                     int64_t max_pages, const int32_t *lengths, float scale, void *out,
+                     int64_t o_token, int64_t o_head, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+  if (batch < 0 || batch > INT32_MAX || heads < 1 || heads > kMaxHeads || kv_heads < 1 ||
+      kv_heads > heads || heads % kv_heads || !float_dtype(dtype) || max_pages < 0 ||
+      max_pages > INT32_MAX || ld_table < 0 || !(scale > 0.0f) || !(scale < INFINITY))
+    return DLRM_ERR_SHAPE;
+  const int bad = cache_shape(kv_heads, dim, pages, page, bits);
+  if (bad) return bad;
+  if (!in_rows(q_token, q_head) || !out_rows(batch, heads, dim, o_token, o_head))
+    return DLRM_ERR_SHAPE;
+  if (batch == 0) return DLRM_OK;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || (max_pages > 0 && !table) ||
+      !lengths || !out)
+    return DLRM_ERR_NULL;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales))
+    return DLRM_ERR_UNSUPPORTED;
+  const size_t need = cached_workspace(batch, heads, kv_heads, dim, max_pages, page);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return DLRM_ERR_WORKSPACE;
+  CachedParams p{};
+  p.batch = batch;
+  p.pages = pages;
+  p.max_pages = max_pages;
+  p.heads = heads;
+  p.group = heads / kv_heads;
+  p.page = page;
+  p.q = {q, q_token, q_head};
+  p.k_codes = (const uint8_t *)k_codes;
+  p.k_scales = (const uint8_t *)k_scales;
+  p.v_codes = (const uint8_t *)v_codes;
+  p.v_scales = (const uint8_t *)v_scales;
+  p.table = table;
+  p.ld_table = ld_table;
+  p.lengths = lengths;
+  p.scale = scale;
+  p.out = {out, o_token, o_head};
+  return status_of(launch_cached(p, dtype, dim, bits, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -339,4 +339,35 @@ size_t attention_grad_workspace(int64_t tokens, int heads);
 hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *ws,
                                  hipStream_t stream);
 
+// Paged cache in 8 or 4 bits (kv_cache.hip): codes (pages, heads, page, dim *
+// bits / 8), scales (pages, heads, page, dim / 32).
+struct CacheParams {
+  int64_t tokens, pages;
+  int heads, dim, page;
+  const int32_t *slots;  // (tokens,)
+  const void *k, *v;     // written
+  void *out_k, *out_v;   // or read
+  int64_t k_token, k_head, v_token, v_head;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+};
+hipError_t launch_cache_write(const CacheParams &p, int dtype, int bits, hipStream_t stream);
+hipError_t launch_cache_read(const CacheParams &p, int dtype, int bits, hipStream_t stream);
+
+// Attention of single tokens over it (attention_cached.hip).
+struct CachedParams {
+  int64_t batch, pages, max_pages;
+  int heads, group, page;
+  HeadRows q;  // (batch, heads, dim)
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int32_t *table;  // (batch, max_pages), rows ld_table apart
+  int64_t ld_table;
+  const int32_t *lengths;  // (batch,)
+  float scale;
+  HeadRowsOut out;
+};
+size_t cached_workspace(int64_t batch, int heads, int kv_heads, int dim, int64_t max_pages,
+                        int page);
+hipError_t launch_cached(const CachedParams &p, int dtype, int dim, int bits, void *ws,
+                         hipStream_t stream);
+
 }  // namespace dlrm

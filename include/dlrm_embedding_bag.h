@@ -808,6 +808,86 @@ DLRM_API int attention_packed_grad(
     int64_t dk_token, int64_t dk_head, void *dv, int64_t dv_token, int64_t dv_head,
     void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * A cache of keys and values in pages, held in 8 or 4 bits: four arrays, each on
+ * 16 bytes and contiguous,
+ *   k_codes, v_codes    (pages, heads, page, dim * bits / 8) bytes
+ *   k_scales, v_scales  (pages, heads, page, dim / 32) bytes
+ * Row `slot` of a head is row slot % page of page slot / page.  32 neighbouring
+ * values of a row share a scale byte s and stand for code * 2^(s - 127): codes
+ * are FP8 E4M3 in 8 bits, and in 4 bits E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ * sign), the first of two in the lower half byte.  A scale of 255 stands for NaN.
+ *   dim    32, 64 or 128; bits 4 or 8; page a power of two from 16 to
+ *          DLRM_MAX_CACHE_PAGE (else DLRM_ERR_UNSUPPORTED)
+ *   pages  >= 1, pages * page <= INT32_MAX
+ */
+#define DLRM_MAX_CACHE_PAGE 4096
+
+/*
+ * kv_cache_write -- token t's keys and values into row slots[t] of all heads.  A
+ * group's scale is the smallest 2^e, e >= -117, that clips none of its values
+ * (448 * 2^e or 6 * 2^e is at least the largest magnitude); codes are rounded to
+ * nearest, ties to even.  Magnitudes beyond 1.75 * 2^127 in 8 bits, or 1.5 * 2^127
+ * in 4, are clipped to them, so that no finite value is read back as an infinity.  A group that holds an infinity or a NaN gets scale 255
+ * and codes 0.
+ *
+ *   tokens   0 <= tokens <= INT32_MAX (0: nothing to do)
+ *   k, v     (tokens, heads, dim) of dtype, strides of tokens and heads
+ *   slots    (tokens,) int32; a token whose slot lies outside [0, pages * page)
+ *            (padding, usually -1) is not written.  A slot that is named twice
+ *            holds codes and scales of either token, not of one
+ */
+DLRM_API int kv_cache_write(int64_t tokens, int32_t heads, int32_t dim, int32_t dtype,
+                            const void *k, int64_t k_token, int64_t k_head, const void *v,
+                            int64_t v_token, int64_t v_head, const int32_t *slots, int64_t pages,
+                            int32_t page, int32_t bits, void *k_codes, void *k_scales,
+                            void *v_codes, void *v_scales, void *stream);
+
+/*
+ * kv_cache_read -- the values that rows slots[t] stand for, zeros for a slot
+ * outside [0, pages * page): exact in dtype (float32, bfloat16) for what
+ * kv_cache_write wrote.
+ */
+DLRM_API int kv_cache_read(int64_t tokens, int32_t heads, int32_t dim, int32_t dtype,
+                           const int32_t *slots, int64_t pages, int32_t page, int32_t bits,
+                           const void *k_codes, const void *k_scales, const void *v_codes,
+                           const void *v_scales, void *k, int64_t k_token, int64_t k_head, void *v,
+                           int64_t v_token, int64_t v_head, void *stream);
+
+/*
+ * attention_cached -- attention_packed of one query for each sequence over the
+ * cache: with the keys and values that the rows stand for,
+ *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k[j]) v[j],  j < lengths[b]
+ * Key j of sequence b is row j % page of page table[b, j / page].  Keys of a page
+ * outside [0, pages) are not there; a sequence without keys has out 0.  What lies
+ * in a page behind a sequence's last key does not reach it.  For bfloat16
+ * queries the weights are rounded to bfloat16 before they meet the values; out is
+ * rounded once.
+ *
+ *   batch    0 <= batch <= INT32_MAX (0: nothing to do)
+ *   heads    a multiple of kv_heads, the cache's heads
+ *   q, out   (batch, heads, dim) of dtype, strides of sequences and heads
+ *   table    (batch, max_pages) int32, row stride ld_table (0: one row for all)
+ *   lengths  (batch,) int32, at most max_pages * page (what lies beyond is not
+ *            there)
+ *   scale    finite, > 0
+ *   workspace  16-byte aligned, at least attention_cached_workspace_bytes bytes
+ *              (which may return 0, and does for sizes that the call refuses); it
+ *              needs no clearing.  Its size and the split of the work depend on
+ *              max_pages, not on the lengths, so a captured call follows lengths
+ *              that change in place
+ */
+DLRM_API size_t attention_cached_workspace_bytes(int64_t batch, int32_t heads, int32_t kv_heads,
+                                                 int32_t dim, int64_t max_pages, int32_t page);
+DLRM_API int attention_cached(int64_t batch, int32_t heads, int32_t kv_heads, int32_t dim,
+                              int32_t dtype, const void *q, int64_t q_token, int64_t q_head,
+                              int64_t pages, int32_t page, int32_t bits, const void *k_codes,
+                              const void *k_scales, const void *v_codes, const void *v_scales,
+                              const int32_t *table, int64_t ld_table, int64_t max_pages,
+                              const int32_t *lengths, float scale, void *out, int64_t o_token,
+                              int64_t o_head, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
 #ifdef __cplusplus
 }
 #endif

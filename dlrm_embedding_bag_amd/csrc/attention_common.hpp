@@ -120,86 +120,127 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t f
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds, 4, from, 0, 0, 0);
 }
 
+// A value that every lane of the wave holds alike, for the scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
 // What a thread asks for when a tile is filled: where its chunks lie in memory,
-// relative to the tile's first row.
+// relative to the first row of each load.
 template <typename T, int ROWS, int DP, int WAVES>
 struct TileLoad {
+  using S = typename T::S;
   using L = LdsTile<T, ROWS, DP>;
   static constexpr int LOADS = L::SIZE / (WAVES * kWave);
-  static_assert(L::SIZE % (WAVES * kWave) == 0);
-  static constexpr uint32_t kNowhere = 0x80000000u;  // beyond any tile: reads as zeros
-  uint32_t from[LOADS];
+  static constexpr int STEP = WAVES * kWave / L::C;   // rows of a load
+  static constexpr int KINDS = STEP % 8 ? LOADS : 1;  // keys repeat every eight rows
+  static_assert(L::SIZE % (WAVES * kWave) == 0 && WAVES * kWave % L::C == 0);
+  static constexpr uint32_t kNowhere = 0x80000000u;   // beyond any tile: reads as zeros
+  uint32_t from[KINDS];
 
   __device__ __forceinline__ TileLoad(int wave, int lane, int64_t row_stride, int dim) {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int at = (i * WAVES + wave) * kWave + lane;
-      const int r = at / L::C, c = ((at % L::C) ^ L::key(r)) * L::E;
-      from[i] = c < dim ? (uint32_t)((r * row_stride + c) * (int64_t)sizeof(typename T::S))
-                        : kNowhere;
+    for (int i = 0; i < KINDS; ++i) {
+      const int at = wave * kWave + lane, r = at / L::C;
+      const int c = ((at % L::C) ^ L::key(i * STEP + r)) * L::E;
+      from[i] = c < dim ? (uint32_t)((r * row_stride + c) * (int64_t)sizeof(S)) : kNowhere;
     }
   }
   // Rows `base` on, of which `rows` are there (the others become zeros); the
   // loads are on their way when this returns.
-  __device__ __forceinline__ void fill(u32x4_t *lds, const typename T::S *base, int64_t rows,
-                                       int64_t row_stride, int dim, int wave) const {
-    const int n = rows < ROWS ? (int)rows : ROWS;
-    const uint32_t bytes =
-        n > 0 ? (uint32_t)(((n - 1) * row_stride + dim) * (int64_t)sizeof(typename T::S)) : 0;
-    const auto b = buffer_of(base, bytes);
+  __device__ __forceinline__ void fill(u32x4_t *lds, const S *base, int rows, int64_t row_stride,
+                                       int dim, int wave) const {
+    const int n = rows < ROWS ? rows : ROWS;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load_to_lds(b, from[i], lds + (i * WAVES + wave) * kWave);
+    for (int i = 0; i < LOADS; ++i) {
+      const int left = n - i * STEP;
+      const uint32_t bytes =
+          left > 0 ? (uint32_t)((left - 1) * (uint32_t)row_stride + dim) * (uint32_t)sizeof(S) : 0;
+      load_to_lds(buffer_of(base + i * STEP * row_stride, bytes), from[KINDS == 1 ? 0 : i],
+                  lds + (i * WAVES + wave) * kWave);
+    }
   }
 };
+
+// What a lane reads of tiles: the places of its own row, or of its own columns,
+// at any of which the rest of an address is a constant.  (The key touches three
+// bits of a chunk's number, so few places serve all reads.)
+typedef const __attribute__((address_space(3))) char *LdsBytes;
+template <typename V>
+__device__ __forceinline__ V lds_at(const u32x4_t *lds, uint32_t place) {
+  return *(const __attribute__((address_space(3))) V *)((LdsBytes)lds + place);
+}
 
 // Row r0 + lane % 32 of a tile, elements 16 step + 8 (lane / 32) on: the operand
 // of a product over the row's elements.
 template <typename T, int ROWS, int DP>
-__device__ __forceinline__ Operand<T> read_rows(const u32x4_t *lds, int r0, int step, int lane) {
+struct ReadRows {
   using L = LdsTile<T, ROWS, DP>;
-  const int r = lane & 31, h = lane >> 5;
-  const u32x4_t *row = lds + (r0 + r) * L::C;
-  Operand<T> o;
-  if constexpr (L::E == 8) {
-    o.v = row[(step * 2 + h) ^ L::key(r)];
-  } else {
+  uint32_t place[4];
+  __device__ __forceinline__ explicit ReadRows(int lane) {
+    const int r = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      o.v[e] = __builtin_bit_cast(f32x4_t, row[(step * 4 + h * 2 + e) ^ L::key(r)]);
+    for (int i = 0; i < 4; ++i) {
+      const int c = L::E == 8 ? i * 2 + h : (i >> 1) * 4 + h * 2 + (i & 1);
+      place[i] = (uint32_t)(r * L::C + ((c ^ L::key(r)) & (L::C - 1))) * 16;
+    }
   }
-  return o;
-}
+  __device__ __forceinline__ Operand<T> read(const u32x4_t *lds, int r0, int step) const {
+    Operand<T> o;
+    if constexpr (L::E == 8) {
+      o.v = lds_at<u32x4_t>(lds, place[step & 3] + (r0 * L::C + (step >> 2) * 8) * 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        o.v[e] = lds_at<f32x4_t>(
+            lds, place[(step & 1) * 2 + e] + (r0 * L::C + (step >> 1) * 8) * 16);
+    }
+    return o;
+  }
+};
 
-// Column d0 + lane % 32 of a tile, its rows r0 + row_of(e, lane / 32) in slots e
+// Column 32 d + lane % 32 of a tile, its rows r0 + row_of(e, lane / 32) in slots e
 // of 0..7: the operand of a product over 16 rows (r0 a multiple of 16).  For
 // bfloat16 by the transposing read: of 16 lanes each gives the place of four
 // elements, and gets one element of each of the four rows they span.
 template <typename T, int ROWS, int DP>
-__device__ __forceinline__ Operand<T> read_columns(const u32x4_t *lds, int r0, int d0, int lane) {
+struct ReadColumns {
   using L = LdsTile<T, ROWS, DP>;
-  Operand<T> o;
-  const int h = lane >> 5;
-  if constexpr (L::E == 8) {
-    typedef __attribute__((address_space(3))) i16x4_t *Quad;
-    const int i = lane & 15;
-    const int c = d0 / 8 + (lane >> 4 & 1) * 2 + (i >> 1 & 1);
-    const int t = h * 4 + (i >> 2);
-    const char *at = (const char *)(lds + (r0 + t) * L::C + (c ^ L::key(t))) + (i & 1) * 8;
-    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)at);
-    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)(at + 8 * L::C * 16));
-    const auto a = __builtin_bit_cast(u32x2_u, lo), b = __builtin_bit_cast(u32x2_u, hi);
-    o.v = u32x4_t{a[0], a[1], b[0], b[1]};
-  } else {
-    const int d = d0 + (lane & 31);
+  static constexpr int N = L::E == 8 ? 2 : 4;
+  uint32_t place[N];
+  __device__ __forceinline__ explicit ReadColumns(int lane) {
+    const int h = lane >> 5;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int t = row_of(e, h);
-      o.v[e >> 2][e & 3] =
-          reinterpret_cast<const float *>(lds + (r0 + t) * L::C + ((d >> 2) ^ L::key(t)))[d & 3];
+    for (int i = 0; i < N; ++i) {
+      if constexpr (L::E == 8) {
+        const int q = lane & 15, t = h * 4 + (q >> 2);
+        const int c = i * 4 + (lane >> 4 & 1) * 2 + (q >> 1 & 1);
+        place[i] = (uint32_t)(t * L::C + ((c ^ L::key(t)) & (L::C - 1))) * 16 + (q & 1) * 8;
+      } else {
+        const int t = h * 4 + i, c = (lane & 31) >> 2;
+        place[i] = (uint32_t)(t * L::C + (c ^ L::key(t))) * 16 + (lane & 3) * 4;
+      }
     }
   }
-  return o;
-}
+  __device__ __forceinline__ Operand<T> read(const u32x4_t *lds, int r0, int d) const {
+    Operand<T> o;
+    if constexpr (L::E == 8) {
+      typedef __attribute__((address_space(3))) i16x4_t *Quad;
+      const LdsBytes at = (LdsBytes)lds + (place[d & 1] + (r0 * L::C + (d >> 1) * 8) * 16);
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)at);
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)(at + 8 * L::C * 16));
+      const auto a = __builtin_bit_cast(u32x2_u, lo), b = __builtin_bit_cast(u32x2_u, hi);
+      o.v = u32x4_t{a[0], a[1], b[0], b[1]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o.v[e >> 2][e & 3] = lds_at<float>(
+            lds, place[e & 3] + ((r0 + (e >> 2) * 8) * L::C + d * 8) * 16);
+    }
+    return o;
+  }
+};
 
 // Loads to LDS and LDS accesses of this wave are done, and everyone's.
 __device__ __forceinline__ void landed() {
@@ -217,9 +258,9 @@ __device__ __forceinline__ void landed() {
 // (a few too many), grows with s, and takes no table.  A tile is found by a
 // search for its segment, 64 at a time.
 struct Tile {
-  int64_t sequence;     // -1: outside all sequences
-  int64_t first, last;  // rows of the segment
-  int64_t row;          // first row of the tile; none where it is >= last
+  int sequence;     // -1: outside all sequences
+  int first, row;   // rows: the segment's first, the tile's first
+  int left;         // rows from there to the segment's end; none where it is <= 0
 };
 
 // Where segment s begins, and the last one ends; offsets that a bad array holds
@@ -252,48 +293,51 @@ __device__ __forceinline__ Tile find_tile(const int32_t *offsets, int64_t batch,
     lo += last * step;
     n = end - lo < step ? end - lo : step;
   }
-  lo = (int64_t)__builtin_amdgcn_readfirstlane((uint32_t)lo) |
-       (int64_t)__builtin_amdgcn_readfirstlane((uint32_t)(lo >> 32)) << 32;
+  lo = uniform(lo);
+  const int64_t first = uniform(segment_start(offsets, batch, total, lo));
+  const int64_t last = uniform(segment_start(offsets, batch, total, lo + 1));
+  const int64_t k = tile - (first / rows + lo);
+  const int64_t row = k < 0 ? last : first + k * rows;
   Tile t;
-  t.sequence = lo >= 1 && lo <= batch ? lo - 1 : -1;
-  t.first = segment_start(offsets, batch, total, lo);
-  t.last = segment_start(offsets, batch, total, lo + 1);
-  const int64_t k = tile - (t.first / rows + lo);
-  t.row = k < 0 ? t.last : t.first + k * rows;
+  t.sequence = lo >= 1 && lo <= batch ? (int)lo - 1 : -1;
+  t.first = (int)first;
+  t.left = row < last ? (int)(last - row) : 0;
+  t.row = (int)(row < last ? row : last);
   return t;
 }
 
-// The keys of a tile's sequence.
-struct KeyRange {
-  int64_t first, count;
+// The rows of sequence b in the other tensor.
+struct Range {
+  int first, count;
 };
-__device__ __forceinline__ KeyRange keys_of(const int32_t *offsets, const int32_t *kv_offsets,
-                                            int64_t batch, int64_t kv_tokens, const Tile &t) {
-  if (!kv_offsets) return {t.first, t.last - t.first};
-  const int64_t first = segment_start(kv_offsets, batch, kv_tokens, t.sequence + 1);
-  const int64_t last = segment_start(kv_offsets, batch, kv_tokens, t.sequence + 2);
+__device__ __forceinline__ Range rows_of(const int32_t *offsets, int64_t batch, int64_t total,
+                                         int b) {
+  const int first = uniform((int)segment_start(offsets, batch, total, (int64_t)b + 1));
+  const int last = uniform((int)segment_start(offsets, batch, total, (int64_t)b + 2));
   return {first, last > first ? last - first : 0};
 }
 
-// How many of them, from the first on, are seen: all, or with `causal` by the
-// last row all and by each row before it one less.
+// How many keys, from the first on, are seen: all, or with `causal` by the last
+// row all and by each row before it one less.  Rows count from the tile's first.
 struct SeenKeys {
-  int64_t mine;      // by this lane's row
-  int64_t wave_all;  // by every row of the wave's 32
-  int64_t wave_any;  // by any of them
-  int64_t tile_any;  // by any row of the workgroup's tile
-  __device__ __forceinline__ SeenKeys(int causal, int64_t keys, int64_t last, int64_t tile_row,
-                                      int tile_rows, int wave, int64_t row, bool there) {
-    auto by = [&](int64_t r) {
-      const int64_t n = causal ? keys - (last - 1 - r) : keys;
+  int wave_all;  // by every row of the wave's 32 (that is there)
+  int wave_any;  // by any of them
+  int tile_all;  // by every row of the workgroup's tile
+  int tile_any;  // by any of them
+  int mine;      // by this lane's row
+  __device__ __forceinline__ SeenKeys(bool causal, int keys, int rows_left, int tile_rows, int wave,
+                                      int lane) {
+    auto by = [&](int r) {
+      const int n = causal ? keys - (rows_left - 1 - r) : keys;
       return n < 0 ? 0 : n;
     };
-    auto end = [&](int64_t r) { return r < last - 1 ? r : last - 1; };
-    const int64_t first = tile_row + wave * 32;
-    mine = there ? by(row) : 0;
-    wave_all = first + 31 < last ? by(first) : 0;
-    wave_any = first < last ? by(end(first + 31)) : 0;
-    tile_any = by(end(tile_row + tile_rows - 1));
+    auto end = [&](int r) { return r < rows_left - 1 ? r : rows_left - 1; };
+    const int first = wave * 32, row = first + (lane & 31);
+    mine = row < rows_left ? by(row) : 0;
+    wave_all = first < rows_left ? by(first) : 0;
+    wave_any = first < rows_left ? by(end(first + 31)) : 0;
+    tile_all = by(0);
+    tile_any = by(end(tile_rows - 1));
   }
 };
 

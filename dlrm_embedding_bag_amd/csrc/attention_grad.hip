@@ -73,27 +73,32 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_rows_kernel(AttentionGradPa
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
   const TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
+  const ReadRows<T, BN, DP> by_row(lane);
+  const ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t tile = item / p.heads;
     const int head = (int)(item - tile * p.heads);
     const Tile t = find_tile(p.offsets, p.batch, p.tokens, tile, BM);
-    if (t.row >= t.last) continue;
-    const int64_t row = t.row + wave * 32 + (lane & 31);
-    const bool there = row < t.last;
-    S *dq = (S *)p.dq.data + row * p.dq.token + head * p.dq.head;
+    if (t.left <= 0) continue;
+    const int mine = wave * 32 + (lane & 31);   // row of the tile
+    const int64_t row = (int64_t)t.row + mine;
+    const bool there = mine < t.left;
     if (t.sequence < 0) {
-      if (there && half == 0 && p.fill & 1)
+      if (there && half == 0 && p.fill & 1) {
+        S *dq = (S *)p.dq.data + row * p.dq.token + head * p.dq.head;
         for (int d = 0; d < p.dim; ++d) dq[d] = 0;
+      }
       continue;
     }
-    const KeyRange range = keys_of(p.offsets, p.kv_offsets, p.batch, p.kv_tokens, t);
-    const SeenKeys seen(p.causal, range.count, t.last, t.row, BM, wave, row, there);
-    const int64_t count = (seen.tile_any + BN - 1) / BN;
+    const Range keys = p.kv_offsets ? rows_of(p.kv_offsets, p.batch, p.kv_tokens, t.sequence)
+                                    : Range{t.first, t.row - t.first + t.left};
+    const SeenKeys seen(p.causal != 0, keys.count, t.left, BM, wave, lane);
+    const int count = seen.tile_any / BN + (seen.tile_any % BN != 0);
     const int kv_head = head / p.group;
-    const S *kbase = (const S *)p.k.data + range.first * p.k.token + kv_head * p.k.head;
-    const S *vbase = (const S *)p.v.data + range.first * p.v.token + kv_head * p.v.head;
+    const S *kbase = (const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head;
+    const S *vbase = (const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head;
 
     Operand<T> q[STEPS], g[STEPS];
     float delta = 0.0f;
@@ -117,22 +122,24 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_rows_kernel(AttentionGradPa
     f32x16_t o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
-    auto fill = [&](u32x4_t *k, u32x4_t *v, int64_t n) {
-      kload.fill(k, kbase + n * BN * p.k.token, range.count - n * BN, p.k.token, p.dim, wave);
-      vload.fill(v, vbase + n * BN * p.v.token, range.count - n * BN, p.v.token, p.dim, wave);
+    auto fill = [&](u32x4_t *k, u32x4_t *v, int n) {
+      kload.fill(k, kbase + (int64_t)n * BN * p.k.token, keys.count - n * BN, p.k.token, p.dim,
+                 wave);
+      vload.fill(v, vbase + (int64_t)n * BN * p.v.token, keys.count - n * BN, p.v.token, p.dim,
+                 wave);
     };
-    auto work = [&](const u32x4_t *k, const u32x4_t *v, int64_t n) {
-      const int64_t base = n * BN;
+    auto work = [&](const u32x4_t *k, const u32x4_t *v, int n) {
+      const int base = n * BN;
       if (base >= seen.wave_any) return;
-      const bool masked = base + BN > seen.wave_all;
-      const int left = (int)(seen.mine - base < BN ? seen.mine - base : BN);
+      const bool masked = seen.wave_all - base < BN;
+      const int left = seen.mine - base;
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
         f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
         for (int e = 0; e < STEPS; ++e) {
-          s = multiply(read_rows<T, BN, DP>(k, j * 32, e, lane), q[e], s);
-          dp = multiply(read_rows<T, BN, DP>(v, j * 32, e, lane), g[e], dp);
+          s = multiply(by_row.read(k, j * 32, e), q[e], s);
+          dp = multiply(by_row.read(v, j * 32, e), g[e], dp);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -147,12 +154,12 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_rows_kernel(AttentionGradPa
           const Operand<T> w = operand_of<T>(s, h);
 #pragma unroll
           for (int d = 0; d < DT; ++d)
-            o[d] = multiply(read_columns<T, BN, DP>(k, j * 32 + h * 16, d * 32, lane), w, o[d]);
+            o[d] = multiply(by_column.read(k, j * 32 + h * 16, d), w, o[d]);
         }
       }
     };
     if (count > 0) fill(k0, v0, 0);
-    for (int64_t n = 0; n < count; n += 2) {
+    for (int n = 0; n < count; n += 2) {
       landed();
       if (n + 1 < count) fill(k1, v1, n + 1);
       work(k0, v0, n);
@@ -163,16 +170,18 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_rows_kernel(AttentionGradPa
       }
     }
     landed();
-    if (there) store_rows<T, DT>(dq, o, p.scale, half, p.dim);
+    if (mine < t.left)
+      store_rows<T, DT>((S *)p.dq.data + ((int64_t)t.row + mine) * p.dq.token + head * p.dq.head,
+                        o, p.scale, half, p.dim);
   }
 }
 
 // The statistics of a tile's rows, 32 a load; behind the last row zeros (whose
 // gradient is zero, too, so they add nothing).
 template <int BN, int WAVES>
-__device__ __forceinline__ void fill_stats(float *lds, const RowStats *stats, int64_t rows,
-                                           int wave, int lane) {
-  const int n = rows < BN ? (int)rows : BN;
+__device__ __forceinline__ void fill_stats(float *lds, const RowStats *stats, int rows, int wave,
+                                           int lane) {
+  const int n = rows < BN ? rows : BN;
   const auto b = buffer_of(stats, (uint32_t)(n * sizeof(RowStats)));
   for (int j = wave; j < BN / 32; j += WAVES)
     load_to_lds(b, (j * kWave + lane) * 4, lds + j * kWave);
@@ -192,6 +201,8 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradPa
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
   const TileLoad<T, BN, DP, WAVES> gload(wave, lane, p.grad.token, p.dim);
+  const ReadRows<T, BN, DP> by_row(lane);
+  const ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
   const int32_t *key_offsets = p.kv_offsets ? p.kv_offsets : p.offsets;
 
@@ -199,13 +210,13 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradPa
     const int64_t tile = item / kv_heads;
     const int kv_head = (int)(item - tile * kv_heads);
     const Tile t = find_tile(key_offsets, p.batch, p.kv_tokens, tile, BM);
-    if (t.row >= t.last) continue;
-    const int64_t key = t.row + wave * 32 + (lane & 31);
-    const bool there = key < t.last;
-    S *dk = (S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head;
-    S *dv = (S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head;
+    if (t.left <= 0) continue;
+    const int mine = wave * 32 + (lane & 31);   // key of the tile
     if (t.sequence < 0) {
-      if (there && half == 0) {
+      if (mine < t.left && half == 0) {
+        const int64_t key = (int64_t)t.row + mine;
+        S *dk = (S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head;
+        S *dv = (S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head;
         for (int d = 0; d < p.dim; ++d) {
           if (p.fill & 2) dk[d] = 0;
           if (p.fill & 4) dv[d] = 0;
@@ -213,30 +224,27 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradPa
       }
       continue;
     }
-    int64_t first = t.first, rows = t.last - t.first;
-    if (p.kv_offsets) {
-      first = segment_start(p.offsets, p.batch, p.tokens, t.sequence + 1);
-      rows = segment_start(p.offsets, p.batch, p.tokens, t.sequence + 2) - first;
-      if (rows < 0) rows = 0;
-    }
-    // the first row that sees a key: as far from the last row as the key from
-    // the last key
-    auto first_row = [&](int64_t at) {
-      const int64_t r = p.causal ? rows - (t.last - at) : 0;
+    const Range rows = p.kv_offsets ? rows_of(p.offsets, p.batch, p.tokens, t.sequence)
+                                    : Range{t.first, t.row - t.first + t.left};
+    // the first row that sees a key of the tile: as far from the last row as the
+    // key from the last key
+    auto first_row = [&](int key) {
+      const int r = p.causal ? rows.count - (t.left - key) : 0;
       return r < 0 ? 0 : r;
     };
-    const int64_t wave_key = t.row + wave * 32;
-    const int64_t wave_end = wave_key + 31 < t.last - 1 ? wave_key + 31 : t.last - 1;
+    const int wave_key = wave * 32;
+    const int wave_end = wave_key + 31 < t.left ? wave_key + 31 : t.left - 1;
     // (a wave without keys has nothing to see)
-    const int64_t wave_from = wave_key < t.last ? first_row(wave_key) : rows;
-    const int64_t wave_full = wave_key < t.last ? first_row(wave_end) : rows;
-    const int64_t mine = there ? first_row(key) : rows;
-    const int64_t n0 = first_row(t.row) / BN;
-    const int64_t per_head = (rows + BN - 1) / BN - n0;
-    const int64_t count = per_head > 0 ? per_head * p.group : 0;
+    const int wave_from = wave_key < t.left ? first_row(wave_key) : rows.count;
+    const int wave_full = wave_key < t.left ? first_row(wave_end) : rows.count;
+    const int from_row = mine < t.left ? first_row(mine) : rows.count;
+    const int n0 = first_row(0) / BN;
+    const int per_head = rows.count / BN + (rows.count % BN != 0) - n0;
 
     Operand<T> k[STEPS], v[STEPS];
     {
+      const int64_t key = (int64_t)t.row + mine;
+      const bool there = mine < t.left;
       const S *kat = (const S *)p.k.data + key * p.k.token + kv_head * p.k.head;
       const S *vat = (const S *)p.v.data + key * p.v.token + kv_head * p.v.head;
 #pragma unroll
@@ -249,27 +257,27 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradPa
 #pragma unroll
     for (int d = 0; d < DT; ++d) ok[d] = ov[d] = f32x16_t{};
 
-    auto fill = [&](u32x4_t *q, u32x4_t *g, float *st, int64_t it) {
-      const int64_t h = it / per_head, n = n0 + it - h * per_head;
-      const int64_t head = kv_head * (int64_t)p.group + h, row = first + n * BN;
-      const int64_t left = rows - n * BN;
+    // tiles of rows, head by head of the group
+    auto fill = [&](u32x4_t *q, u32x4_t *g, float *st, int h, int n) {
+      const int64_t head = (int64_t)kv_head * p.group + h, row = rows.first + (int64_t)n * BN;
+      const int left = rows.count - n * BN;
       qload.fill(q, (const S *)p.q.data + row * p.q.token + head * p.q.head, left, p.q.token,
                  p.dim, wave);
       gload.fill(g, (const S *)p.grad.data + row * p.grad.token + head * p.grad.head, left,
                  p.grad.token, p.dim, wave);
       fill_stats<BN, WAVES>(st, stats + head * p.tokens + row, left, wave, lane);
     };
-    auto work = [&](const u32x4_t *q, const u32x4_t *g, const float *st, int64_t it) {
-      const int64_t n = n0 + it % per_head, base = n * BN;
-      if (base + BN <= wave_from) return;
+    auto work = [&](const u32x4_t *q, const u32x4_t *g, const float *st, int n) {
+      const int base = n * BN;
+      if (wave_from - base >= BN) return;
       const bool masked = base < wave_full;
 #pragma unroll
       for (int j = 0; j < QT; ++j) {
         f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
         for (int e = 0; e < STEPS; ++e) {
-          s = multiply(read_rows<T, BN, DP>(q, j * 32, e, lane), k[e], s);
-          dp = multiply(read_rows<T, BN, DP>(g, j * 32, e, lane), v[e], dp);
+          s = multiply(by_row.read(q, j * 32, e), k[e], s);
+          dp = multiply(by_row.read(g, j * 32, e), v[e], dp);
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradPa
           }
         }
         if (masked) {
-          const int from = mine - base < BN ? (int)(mine - base) : BN;   // rows of the tile before it do not see the key
+          const int from = from_row - base;   // rows of the tile before it do not see the key
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (j * 32 + row_of(i, half) < from) s[i] = dp[i] = 0.0f;
@@ -294,27 +302,46 @@ __global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradPa
           const Operand<T> wp = operand_of<T>(s, h), wd = operand_of<T>(dp, h);
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            ov[d] = multiply(read_columns<T, BN, DP>(g, j * 32 + h * 16, d * 32, lane), wp, ov[d]);
-            ok[d] = multiply(read_columns<T, BN, DP>(q, j * 32 + h * 16, d * 32, lane), wd, ok[d]);
+            ov[d] = multiply(by_column.read(g, j * 32 + h * 16, d), wp, ov[d]);
+            ok[d] = multiply(by_column.read(q, j * 32 + h * 16, d), wd, ok[d]);
           }
         }
       }
     };
-    if (count > 0) fill(q0, g0, s0, 0);
-    for (int64_t n = 0; n < count; n += 2) {
+    int h = 0, n = n0;            // the tile that is worked on
+    int fh = 0, fn = n0;          // the tile that is asked for next
+    auto next = [&](int &hh, int &nn) {
+      if (++nn == n0 + per_head) nn = n0, ++hh;
+    };
+    const bool any = per_head > 0;
+    if (any) {
+      fill(q0, g0, s0, fh, fn);
+      next(fh, fn);
+    }
+    while (any && h < p.group) {
       landed();
-      if (n + 1 < count) fill(q1, g1, s1, n + 1);
-      work(q0, g0, s0, n);
-      if (n + 1 < count) {
-        landed();
-        if (n + 2 < count) fill(q0, g0, s0, n + 2);
-        work(q1, g1, s1, n + 1);
+      if (fh < p.group) {
+        fill(q1, g1, s1, fh, fn);
+        next(fh, fn);
       }
+      work(q0, g0, s0, n);
+      next(h, n);
+      if (h >= p.group) break;
+      landed();
+      if (fh < p.group) {
+        fill(q0, g0, s0, fh, fn);
+        next(fh, fn);
+      }
+      work(q1, g1, s1, n);
+      next(h, n);
     }
     landed();
-    if (there) {
-      store_rows<T, DT>(dk, ok, p.scale, half, p.dim);
-      store_rows<T, DT>(dv, ov, 1.0f, half, p.dim);
+    if (mine < t.left) {
+      const int64_t key = (int64_t)t.row + mine;
+      store_rows<T, DT>((S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head, ok, p.scale, half,
+                        p.dim);
+      store_rows<T, DT>((S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head, ov, 1.0f, half,
+                        p.dim);
     }
   }
 }

@@ -20,125 +20,119 @@
 namespace dlrm {
 namespace {
 
-// Masks of the elements of a word that are not finite.
+// Sign bits of a word's elements that are not finite.
 template <typename T>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  if constexpr (sizeof(typename T::S) == 4)
-    return (w & 0x7f800000u) == 0x7f800000u ? 0xffffffffu : 0u;
-  else
-    return ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u) |
-           ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u);
+  return sizeof(typename T::S) == 4 ? ((w & 0x7fffffffu) + 0x00800000u) & 0x80000000u
+                                    : ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
 }
-template <typename T>
-constexpr int kWords = 8 * (int)sizeof(typename T::S) / 4;  // of an operand
 
-template <typename T>
-__device__ __forceinline__ uint32_t word_of(const Operand<T> &o, int i) {
-  if constexpr (sizeof(typename T::S) == 4)
-    return __float_as_uint(o.v[i >> 2][i & 3]);
-  else
-    return o.v[i];
-}
-template <typename T>
-__device__ __forceinline__ void set_word(Operand<T> &o, int i, uint32_t w) {
-  if constexpr (sizeof(typename T::S) == 4)
-    o.v[i >> 2][i & 3] = __uint_as_float(w);
-  else
-    o.v[i] = w;
-}
-template <typename T>
-__device__ __forceinline__ bool any_not_finite(const Operand<T> &o) {
-  uint32_t bad = 0;
+// A tile of values in LDS: whether it holds one that is not finite, for all
+// waves; if so it is zero there when this returns.
+template <typename T, int SIZE, int WAVES>
+__device__ __forceinline__ bool clean(u32x4_t *v, int *found, int wave, int lane) {
+  constexpr int EACH = SIZE / (WAVES * kWave);
+  uint32_t others = 0;
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) bad |= not_finite<T>(word_of<T>(o, i));
-  return bad != 0;
-}
-// Its finite elements, zeros for the others.
-template <typename T>
-__device__ __forceinline__ Operand<T> finite_part(const Operand<T> &o) {
-  Operand<T> r;
+  for (int i = 0; i < EACH; ++i) {
+    const u32x4_t w = v[(i * WAVES + wave) * kWave + lane];
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i)
-    set_word<T>(r, i, word_of<T>(o, i) & ~not_finite<T>(word_of<T>(o, i)));
-  return r;
-}
-// The element of slot `slot` if it is not finite (and `mine`), zeros elsewhere.
-template <typename T>
-__device__ __forceinline__ Operand<T> other_part(const Operand<T> &o, int slot, bool mine) {
-  Operand<T> r;
-  constexpr int E = 4 / (int)sizeof(typename T::S);
-#pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) {
-    const uint32_t w = word_of<T>(o, i);
-    const uint32_t keep = E == 1 ? 0xffffffffu : slot & 1 ? 0xffff0000u : 0xffffu;
-    set_word<T>(r, i, mine && slot / E == i ? w & not_finite<T>(w) & keep : 0u);
+    for (int e = 0; e < 4; ++e) others |= not_finite<T>(w[e]);
   }
-  return r;
+  const bool mine = __any(others != 0);
+  if (lane == 0) found[wave] = mine;
+  landed();
+  bool any = false;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) any |= found[w] != 0;
+  if (!uniform((int)any)) return false;
+  for (int i = 0; i < EACH; ++i) {
+    u32x4_t *at = v + (i * WAVES + wave) * kWave + lane;
+    u32x4_t w = *at;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t n = not_finite<T>(w[e]);
+      // a sign bit to all bits of its element
+      w[e] &= ~(sizeof(typename T::S) == 4 ? (n ? 0xffffffffu : 0u) : (n >> 15) * 0xffffu);
+    }
+    *at = w;
+  }
+  landed();
+  return true;
 }
 
 template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams p,
+__global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionParams p,
                                                                  int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
   __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[L::SIZE], v1[L::SIZE];
+  __shared__ int found[WAVES];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
   const TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
+  const ReadRows<T, BN, DP> by_row(lane);
+  const ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t tile = item / p.heads;
     const int head = (int)(item - tile * p.heads);
     const Tile t = find_tile(p.offsets, p.batch, p.tokens, tile, BM);
-    if (t.row >= t.last) continue;
-    const int64_t row = t.row + wave * 32 + (lane & 31);
-    const bool there = row < t.last;
-    S *out = (S *)p.out.data + row * p.out.token + head * p.out.head;
+    if (t.left <= 0) continue;
+    const int mine = wave * 32 + (lane & 31);   // row of the tile
     if (t.sequence < 0) {
-      if (there && half == 0 && p.fill & 1)
-        for (int d = 0; d < p.dim; ++d) out[d] = 0;
-      if (there && half == 0 && p.fill & 2) p.lse[row * p.heads + head] = -INFINITY;
+      const int64_t row = (int64_t)t.row + mine;
+      if (mine < t.left && half == 0) {
+        S *out = (S *)p.out.data + row * p.out.token + head * p.out.head;
+        if (p.fill & 1)
+          for (int d = 0; d < p.dim; ++d) out[d] = 0;
+        if (p.fill & 2) p.lse[row * p.heads + head] = -INFINITY;
+      }
       continue;
     }
-    const KeyRange range = keys_of(p.offsets, p.kv_offsets, p.batch, p.kv_tokens, t);
-    const SeenKeys seen(p.causal, range.count, t.last, t.row, BM, wave, row, there);
-    const int64_t count = (seen.tile_any + BN - 1) / BN;
+    const Range keys = p.kv_offsets ? rows_of(p.kv_offsets, p.batch, p.kv_tokens, t.sequence)
+                                    : Range{t.first, t.row - t.first + t.left};
+    const SeenKeys seen(p.causal != 0, keys.count, t.left, BM, wave, lane);
+    const int count = seen.tile_any / BN + (seen.tile_any % BN != 0);
     const int kv_head = head / p.group;
-    const S *kbase = (const S *)p.k.data + range.first * p.k.token + kv_head * p.k.head;
-    const S *vbase = (const S *)p.v.data + range.first * p.v.token + kv_head * p.v.head;
+    const S *kbase = (const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head;
+    const S *vbase = (const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head;
     Operand<T> q[STEPS];
     {
-      const S *at = (const S *)p.q.data + row * p.q.token + head * p.q.head;
+      const S *at = (const S *)p.q.data + ((int64_t)t.row + mine) * p.q.token + head * p.q.head;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
-        q[s] = load_operand<T>(at, s * 16 + half * 8, p.dim, there);
+        q[s] = load_operand<T>(at, s * 16 + half * 8, p.dim, mine < t.left);
     }
     f32x16_t o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
     float m = -INFINITY, l = 0.0f;
+    int loose = -1;   // the first tile whose values are not all added
 
-    auto fill = [&](u32x4_t *k, u32x4_t *v, int64_t n) {
-      kload.fill(k, kbase + n * BN * p.k.token, range.count - n * BN, p.k.token, p.dim, wave);
-      vload.fill(v, vbase + n * BN * p.v.token, range.count - n * BN, p.v.token, p.dim, wave);
+    auto fill = [&](u32x4_t *k, u32x4_t *v, int n) {
+      kload.fill(k, kbase + (int64_t)n * BN * p.k.token, keys.count - n * BN, p.k.token, p.dim,
+                 wave);
+      vload.fill(v, vbase + (int64_t)n * BN * p.v.token, keys.count - n * BN, p.v.token, p.dim,
+                 wave);
     };
-    auto work = [&](const u32x4_t *k, const u32x4_t *v, int64_t n) {
-      const int64_t base = n * BN;
+    auto work = [&](const u32x4_t *k, const u32x4_t *v, int n) {
+      const int base = n * BN;
       if (base >= seen.wave_any) return;
-      const bool masked = base + BN > seen.wave_all;
+      const bool masked = seen.wave_all - base < BN;
       f32x16_t s[KT];
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
         s[j] = f32x16_t{};
 #pragma unroll
         for (int e = 0; e < STEPS; ++e)
-          s[j] = multiply(read_rows<T, BN, DP>(k, j * 32, e, lane), q[e], s[j]);
+          s[j] = multiply(by_row.read(k, j * 32, e), q[e], s[j]);
       }
       if (masked) {
-        const int left = (int)(seen.mine - base < BN ? seen.mine - base : BN);
+        const int left = seen.mine - base;
 #pragma unroll
         for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -168,67 +162,54 @@ __global__ __launch_bounds__(WAVES *kWave) void attention_kernel(AttentionParams
           s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -from));
           l += s[j][i];
         }
-      // A value that is not finite must not reach the rows that do not see it:
-      // zero times it is not zero.  Where a masked tile holds one, the finite
-      // values are added as always and then the others key by key.
-      bool bad = false;
-      if (masked) {
-#pragma unroll
-        for (int j = 0; j < BN / 16; ++j)
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            bad |= any_not_finite<T>(read_columns<T, BN, DP>(v, j * 16, d * 32, lane));
-      }
-      if (__any(bad)) {
-        const int left = (int)(seen.mine - base < BN ? seen.mine - base : BN);
-#pragma unroll
-        for (int j = 0; j < BN / 16; ++j) {
-          const Operand<T> w = operand_of<T>(s[j >> 1], j & 1);
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            o[d] = multiply(finite_part<T>(read_columns<T, BN, DP>(v, j * 16, d * 32, lane)), w,
-                            o[d]);
-          for (int r = 0; r < 16; ++r) {
-            const bool sees = j * 16 + r < left;
-            const int slot = (r >> 3) * 4 + (r & 3);
-            const bool own = (r >> 2 & 1) == half;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const Operand<T> a =
-                  other_part<T>(read_columns<T, BN, DP>(v, j * 16, d * 32, lane), slot, own);
-              if (!__any(any_not_finite<T>(a))) continue;
-              const f32x16_t with = multiply(a, w, o[d]);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[d][i] = sees ? with[i] : o[d][i];
-            }
-          }
-        }
-        return;
-      }
 #pragma unroll
       for (int j = 0; j < BN / 16; ++j) {
         const Operand<T> w = operand_of<T>(s[j >> 1], j & 1);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          o[d] = multiply(read_columns<T, BN, DP>(v, j * 16, d * 32, lane), w, o[d]);
+        for (int d = 0; d < DT; ++d) o[d] = multiply(by_column.read(v, j * 16, d), w, o[d]);
       }
+    };
+    // A value that is not finite must not reach the rows that do not see it, and
+    // zero times it is not zero: from the first tile on that some row does not see
+    // whole, such values are left out, and added after the last tile.
+    auto tile_of = [&](const u32x4_t *k, u32x4_t *v, int n) {
+      if (p.causal && seen.tile_all - n * BN < BN && clean<T, L::SIZE, WAVES>(v, found, wave, lane))
+        loose = loose < 0 ? n : loose;
+      work(k, v, n);
     };
 
     if (count > 0) fill(k0, v0, 0);
-    for (int64_t n = 0; n < count; n += 2) {
+    for (int n = 0; n < count; n += 2) {
       landed();
       if (n + 1 < count) fill(k1, v1, n + 1);
-      work(k0, v0, n);
+      tile_of(k0, v0, n);
       if (n + 1 < count) {
         landed();
         if (n + 2 < count) fill(k0, v0, n + 2);
-        work(k1, v1, n + 1);
+        tile_of(k1, v1, n + 1);
       }
     }
     landed();  // nobody reads the tiles any more
 
+    if (loose >= 0) {   // (weights are above zero, so the values add as they are)
+      for (int j = loose * BN; j < seen.wave_any; ++j) {
+        if (j >= seen.mine) continue;
+        const S *at = vbase + (int64_t)j * p.v.token;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int e = d * 32 + row_of(i, half);
+            const float x = e < p.dim ? load1<T>(at + e) : 0.0f;
+            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[d][i] += x;
+          }
+      }
+    }
+
     l += __uint_as_float(lane_xor<32>(__float_as_uint(l)));
-    if (there) {
+    if (mine < t.left) {
+      const int64_t row = (int64_t)t.row + mine;
+      S *out = (S *)p.out.data + row * p.out.token + head * p.out.head;
       const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
       for (int d = 0; d < DT; ++d)

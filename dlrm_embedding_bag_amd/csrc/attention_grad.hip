@@ -63,7 +63,7 @@ __device__ __forceinline__ float dot(const Operand<T> &a, const Operand<T> &b, f
 
 // Rows: dq, and the rows' statistics.
 template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave) void grad_rows_kernel(AttentionGradParams p,
+__global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGradParams p,
                                                                  RowStats *stats, int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
@@ -189,7 +189,7 @@ __device__ __forceinline__ void fill_stats(float *lds, const RowStats *stats, in
 
 // Keys: dk and dv.  A lane holds one key of its wave's 32.
 template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave) void grad_keys_kernel(AttentionGradParams p,
+__global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGradParams p,
                                                                  const RowStats *stats,
                                                                  int kv_heads, int64_t items) {
   using S = typename T::S;

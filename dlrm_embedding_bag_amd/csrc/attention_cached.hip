@@ -326,26 +326,56 @@ __global__ __launch_bounds__(kWaves *kWave) void cached_kernel(CachedParams p, i
   }
 }
 
-// The shares of a head, one lane an element.
-template <typename T, int D>
-__global__ __launch_bounds__(D) void join_kernel(CachedParams p, int splits, const float *outs,
-                                                 const Share *shares, int64_t items) {
+// The shares of a head: 32 of its elements by GROUPS groups of lanes, each an
+// equal part of the shares.  Few shares take one group (64 sequences of 32 heads,
+// 4 shares: 5 us, with eight groups 10), many take eight (one sequence, 128
+// shares: 7 us, with one group 45).
+constexpr int kJoinThreads = 256;
+template <typename T, int D, int GROUPS>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(CachedParams p, int splits,
+                                                            const float *outs, const Share *shares,
+                                                            int64_t items) {
   using S = typename T::S;
-  const int d = threadIdx.x;
-  for (int64_t row = blockIdx.x; row < items; row += gridDim.x) {
+  constexpr int EACH = kJoinThreads / 32 / GROUPS;   // items of a workgroup
+  __shared__ float parts[GROUPS][32], sums[GROUPS];
+  const int e = threadIdx.x & 31, g = threadIdx.x / 32 % GROUPS;
+  for (int64_t item0 = (int64_t)blockIdx.x * EACH; item0 < items;
+       item0 += (int64_t)gridDim.x * EACH) {
+    int64_t item = item0 + threadIdx.x / 32 / GROUPS;
+    const bool there = item < items;
+    item = there ? item : items - 1;
+    const int64_t row = item / (D / 32);
+    const int d = (int)(item % (D / 32)) * 32 + e;
     const Share *s = shares + row * splits;
     float top = -INFINITY;
-    for (int i = 0; i < splits; ++i) top = fmaxf(top, s[i].top);
+    for (int i = e; i < splits; i += 32) top = fmaxf(top, s[i].top);
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
     float sum = 0.0f, out = 0.0f;
-    for (int i = 0; i < splits; ++i) {
+#pragma unroll 4
+    for (int i = g; i < splits; i += GROUPS) {
       const float f = s[i].top == -INFINITY ? (s[i].sum != 0.0f ? 1.0f : 0.0f)
                                             : __builtin_amdgcn_exp2f(s[i].top - top);
       sum = __builtin_fmaf(s[i].sum, f, sum);
       out = __builtin_fmaf(outs[(row * splits + i) * D + d], f, out);
     }
-    const int64_t b = row / p.heads, h = row - b * p.heads;
-    store1<T>((S *)p.out.data + b * p.out.token + h * p.out.head + d,
-              sum == 0.0f ? 0.0f : out / sum);
+    if constexpr (GROUPS > 1) {
+      parts[g][e] = out;
+      if (e == 0) sums[g] = sum;
+      __syncthreads();
+      sum = out = 0.0f;
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) {
+        sum += sums[i];
+        out += parts[i][e];
+      }
+      __syncthreads();
+    }
+    if (there && g == 0) {
+      const int64_t b = row / p.heads, h = row - b * p.heads;
+      store1<T>((S *)p.out.data + b * p.out.token + h * p.out.head + d,
+                sum == 0.0f ? 0.0f : out / sum);
+    }
   }
 }
 
@@ -359,7 +389,7 @@ int splits_of(int64_t batch, int heads, int kv_heads, int64_t max_pages, int pag
   const int64_t most = (longest + kWaves * kStep - 1) / (kWaves * kStep);
   int64_t want = (2048 + groups - 1) / groups;
   want = want < most ? want : most;
-  want = want < 256 ? want : 256;
+  want = want < 128 ? want : 128;
   return want < 1 ? 1 : (int)want;
 }
 
@@ -374,8 +404,13 @@ hipError_t run(const CachedParams &p, void *ws, hipStream_t stream) {
                 p, splits, tiles, outs, shares, items);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  launch_kernel(join_kernel<T, D>, dim3(grid_of(rows)), dim3(D), 0, stream, p, splits,
-                (const float *)outs, (const Share *)shares, rows);
+  const int64_t pieces = rows * (D / 32);
+  if (splits <= 16)
+    launch_kernel(join_kernel<T, D, 1>, dim3(grid_of((pieces + 7) / 8)), dim3(kJoinThreads), 0,
+                  stream, p, splits, (const float *)outs, (const Share *)shares, pieces);
+  else
+    launch_kernel(join_kernel<T, D, 8>, dim3(grid_of(pieces)), dim3(kJoinThreads), 0, stream, p,
+                  splits, (const float *)outs, (const Share *)shares, pieces);
   return hipGetLastError();
 }
 

@@ -168,7 +168,7 @@ struct TileLoad {
 // bits of a chunk's number, so few places serve all reads.)
 typedef const __attribute__((address_space(3))) char *LdsBytes;
 template <typename V>
-__device__ __forceinline__ V lds_at(const u32x4_t *lds, uint32_t place) {
+__device__ __forceinline__ V lds_at(const void *lds, uint32_t place) {
   return *(const __attribute__((address_space(3))) V *)((LdsBytes)lds + place);
 }
 
@@ -340,6 +340,29 @@ struct SeenKeys {
     tile_any = by(end(tile_rows - 1));
   }
 };
+
+// Item `i` of tiles * heads.  The last tiles come first: with `causal` they see
+// the most keys, and work that ends early should be short (four prompts of up to
+// 6500: X us for Y).  Workgroups go to the eight dies in turn, so a die gets heads
+// that lie together, whose key heads then share its cache.
+struct Item {
+  int64_t tile;
+  int head;
+};
+__device__ __forceinline__ Item item_of(int64_t i, int64_t tiles, int heads) {
+  const uint64_t n = (uint64_t)i;
+  int64_t t;
+  uint32_t r;
+  if (n >> 32) {
+    t = (int64_t)(n / (uint32_t)heads);
+    r = (uint32_t)(n - (uint64_t)t * heads);
+  } else {
+    t = (uint32_t)n / (uint32_t)heads;
+    r = (uint32_t)n - (uint32_t)t * (uint32_t)heads;
+  }
+  if (heads % 8 == 0) r = r % 8 * (heads / 8) + r / 8;
+  return {tiles - 1 - t, (int)r};
+}
 
 // Workgroups for that many items; each takes those a grid apart.
 inline uint32_t grid_of(int64_t items) {

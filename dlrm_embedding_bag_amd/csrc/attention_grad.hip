@@ -20,9 +20,12 @@
 namespace dlrm {
 namespace {
 
-struct RowStats {
-  float lse2;   // of the row in units of log 2; +inf where the row sees nothing
-  float delta;
+// What the second kernel needs of a row, head by head in planes of `tokens`:
+// lse in units of log 2, +inf where the row sees nothing, and then -delta.
+struct Stats {
+  float *lse2, *minus_delta;
+  __host__ __device__ Stats(float *at, int64_t tokens, int64_t heads)
+      : lse2(at), minus_delta(at + tokens * heads) {}
 };
 
 template <typename T, int DT>
@@ -64,11 +67,12 @@ __device__ __forceinline__ float dot(const Operand<T> &a, const Operand<T> &b, f
 // Rows: dq, and the rows' statistics.
 template <typename T, int DP, int WAVES, int BN>
 __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGradParams p,
-                                                                 RowStats *stats, int64_t items) {
+                                                                 float *ws, int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
-  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[L::SIZE], v1[L::SIZE];
+  constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
+  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
@@ -78,9 +82,9 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
   const float c = p.scale * kLog2e;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t tile = item / p.heads;
-    const int head = (int)(item - tile * p.heads);
-    const Tile t = find_tile(p.offsets, p.batch, p.tokens, tile, BM);
+    const Item at = item_of(item, tile_count(p.tokens, p.batch, BM), p.heads);
+    const int head = at.head;
+    const Tile t = find_tile(p.offsets, p.batch, p.tokens, at.tile, BM);
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // row of the tile
     const int64_t row = (int64_t)t.row + mine;
@@ -117,7 +121,11 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
     delta += __uint_as_float(lane_xor<32>(__float_as_uint(delta)));
     float lse2 = there ? p.lse[row * p.heads + head] * kLog2e : INFINITY;
     if (lse2 == -INFINITY) lse2 = INFINITY;
-    if (there && half == 0) stats[(int64_t)head * p.tokens + row] = RowStats{lse2, delta};
+    if (there && half == 0) {
+      const Stats stats(ws, p.tokens, p.heads);
+      stats.lse2[head * p.tokens + row] = lse2;
+      stats.minus_delta[head * p.tokens + row] = -delta;
+    }
 
     f32x16_t o[DT];
 #pragma unroll
@@ -158,45 +166,55 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
         }
       }
     };
-    if (count > 0) fill(k0, v0, 0);
-    for (int n = 0; n < count; n += 2) {
-      landed();
-      if (n + 1 < count) fill(k1, v1, n + 1);
-      work(k0, v0, n);
-      if (n + 1 < count) {
+    if constexpr (WAVES == 1) {
+      for (int n = 0; n < count; ++n) {
+        fill(k0, v0, n);
         landed();
-        if (n + 2 < count) fill(k0, v0, n + 2);
-        work(k1, v1, n + 1);
+        work(k0, v0, n);
+        landed();
       }
+    } else {
+      if (count > 0) fill(k0, v0, 0);
+      for (int n = 0; n < count; n += 2) {
+        landed();
+        if (n + 1 < count) fill(k1, v1, n + 1);
+        work(k0, v0, n);
+        if (n + 1 < count) {
+          landed();
+          if (n + 2 < count) fill(k0, v0, n + 2);
+          work(k1, v1, n + 1);
+        }
+      }
+      landed();
     }
-    landed();
     if (mine < t.left)
       store_rows<T, DT>((S *)p.dq.data + ((int64_t)t.row + mine) * p.dq.token + head * p.dq.head,
                         o, p.scale, half, p.dim);
   }
 }
 
-// The statistics of a tile's rows, 32 a load; behind the last row zeros (whose
+// The statistics of a tile's rows, 64 a load; behind the last row zeros (whose
 // gradient is zero, too, so they add nothing).
 template <int BN, int WAVES>
-__device__ __forceinline__ void fill_stats(float *lds, const RowStats *stats, int rows, int wave,
-                                           int lane) {
+__device__ __forceinline__ void fill_stats(float *lds, const Stats &stats, int64_t at, int rows,
+                                           int wave, int lane) {
+  static_assert(BN <= kWave);
   const int n = rows < BN ? rows : BN;
-  const auto b = buffer_of(stats, (uint32_t)(n * sizeof(RowStats)));
-  for (int j = wave; j < BN / 32; j += WAVES)
-    load_to_lds(b, (j * kWave + lane) * 4, lds + j * kWave);
+  if (wave == 0) load_to_lds(buffer_of(stats.lse2 + at, n * 4), lane * 4, lds);
+  if (wave == WAVES - 1) load_to_lds(buffer_of(stats.minus_delta + at, n * 4), lane * 4, lds + kWave);
 }
 
 // Keys: dk and dv.  A lane holds one key of its wave's 32.
 template <typename T, int DP, int WAVES, int BN>
 __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGradParams p,
-                                                                 const RowStats *stats,
-                                                                 int kv_heads, int64_t items) {
+                                                                 float *ws, int kv_heads,
+                                                                 int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, QT = BN / 32, STEPS = DP / 16, DT = DP / 32;
-  __shared__ u32x4_t q0[L::SIZE], g0[L::SIZE], q1[L::SIZE], g1[L::SIZE];
-  __shared__ float s0[BN * 2], s1[BN * 2];
+  constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
+  __shared__ u32x4_t q0[L::SIZE], g0[L::SIZE], q1[SECOND], g1[SECOND];
+  __shared__ float s0[2 * kWave], s1[2 * kWave];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
@@ -205,11 +223,15 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
   const ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
   const int32_t *key_offsets = p.kv_offsets ? p.kv_offsets : p.offsets;
+  const Stats stats(ws, p.tokens, p.heads);
+  const uint32_t by_stat = half * 16;   // of the lane's first four rows; the others 8 apart
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t tile = item / kv_heads;
-    const int kv_head = (int)(item - tile * kv_heads);
-    const Tile t = find_tile(key_offsets, p.batch, p.kv_tokens, tile, BM);
+    // (the first keys, which most rows see, come first)
+    const int64_t tiles = tile_count(p.kv_tokens, p.batch, BM);
+    const Item at = item_of(item, tiles, kv_heads);
+    const int kv_head = at.head;
+    const Tile t = find_tile(key_offsets, p.batch, p.kv_tokens, tiles - 1 - at.tile, BM);
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // key of the tile
     if (t.sequence < 0) {
@@ -265,7 +287,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
                  p.dim, wave);
       gload.fill(g, (const S *)p.grad.data + row * p.grad.token + head * p.grad.head, left,
                  p.grad.token, p.dim, wave);
-      fill_stats<BN, WAVES>(st, stats + head * p.tokens + row, left, wave, lane);
+      fill_stats<BN, WAVES>(st, stats, head * p.tokens + row, left, wave, lane);
     };
     auto work = [&](const u32x4_t *q, const u32x4_t *g, const float *st, int n) {
       const int base = n * BN;
@@ -273,24 +295,23 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
       const bool masked = base < wave_full;
 #pragma unroll
       for (int j = 0; j < QT; ++j) {
-        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+        f32x16_t s = f32x16_t{}, dp;
 #pragma unroll
-        for (int e = 0; e < STEPS; ++e) {
-          s = multiply(by_row.read(q, j * 32, e), k[e], s);
-          dp = multiply(by_row.read(g, j * 32, e), v[e], dp);
-        }
+        for (int e = 0; e < STEPS; ++e) s = multiply(by_row.read(q, j * 32, e), k[e], s);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const f32x4_t *at =
-              reinterpret_cast<const f32x4_t *>(st + 2 * (j * 32 + row_of(i, half)));
-          const f32x4_t a = at[0], b = at[1];
-          const float lse2[4] = {a[0], a[2], b[0], b[2]}, delta[4] = {a[1], a[3], b[1], b[3]};
+          const f32x4_t lse2 = lds_at<f32x4_t>(st, by_stat + (j * 32 + i * 2) * 4);
+          const f32x4_t from = lds_at<f32x4_t>(st, by_stat + (kWave + j * 32 + i * 2) * 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -lse2[e]));
-            dp[i + e] = s[i + e] * (dp[i + e] - delta[e]);
+            dp[i + e] = from[e];
           }
         }
+#pragma unroll
+        for (int e = 0; e < STEPS; ++e) dp = multiply(by_row.read(g, j * 32, e), v[e], dp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[i] *= s[i];
         if (masked) {
           const int from = from_row - base;   // rows of the tile before it do not see the key
 #pragma unroll
@@ -313,29 +334,39 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
     auto next = [&](int &hh, int &nn) {
       if (++nn == n0 + per_head) nn = n0, ++hh;
     };
-    const bool any = per_head > 0;
-    if (any) {
-      fill(q0, g0, s0, fh, fn);
-      next(fh, fn);
-    }
-    while (any && h < p.group) {
-      landed();
-      if (fh < p.group) {
-        fill(q1, g1, s1, fh, fn);
-        next(fh, fn);
+    const int heads = per_head > 0 ? p.group : 0;
+    if constexpr (WAVES == 1) {
+      while (h < heads) {
+        fill(q0, g0, s0, h, n);
+        landed();
+        work(q0, g0, s0, n);
+        landed();
+        next(h, n);
       }
-      work(q0, g0, s0, n);
-      next(h, n);
-      if (h >= p.group) break;
-      landed();
-      if (fh < p.group) {
+    } else {
+      if (heads) {
         fill(q0, g0, s0, fh, fn);
         next(fh, fn);
       }
-      work(q1, g1, s1, n);
-      next(h, n);
+      while (h < heads) {
+        landed();
+        if (fh < heads) {
+          fill(q1, g1, s1, fh, fn);
+          next(fh, fn);
+        }
+        work(q0, g0, s0, n);
+        next(h, n);
+        if (h >= heads) break;
+        landed();
+        if (fh < heads) {
+          fill(q0, g0, s0, fh, fn);
+          next(fh, fn);
+        }
+        work(q1, g1, s1, n);
+        next(h, n);
+      }
+      landed();
     }
-    landed();
     if (mine < t.left) {
       const int64_t key = (int64_t)t.row + mine;
       store_rows<T, DT>((S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head, ok, p.scale, half,
@@ -347,12 +378,12 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
 }
 
 template <typename T, int DP, int WAVES, int BN>
-hipError_t run(const AttentionGradParams &p, RowStats *stats, hipStream_t stream) {
+hipError_t run(const AttentionGradParams &p, float *ws, hipStream_t stream) {
   const dim3 block(WAVES * kWave);
   if (p.tokens) {
     const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
     launch_kernel(grad_rows_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), block, 0, stream, p,
-                  stats, items);
+                  ws, items);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -360,31 +391,31 @@ hipError_t run(const AttentionGradParams &p, RowStats *stats, hipStream_t stream
   const int kv_heads = p.heads / p.group;
   const int64_t items = tile_count(p.kv_tokens, p.batch, WAVES * 32) * kv_heads;
   launch_kernel(grad_keys_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), block, 0, stream, p,
-                (const RowStats *)stats, kv_heads, items);
+                ws, kv_heads, items);
   return hipGetLastError();
 }
 
 template <typename T, int WAVES, int BN>
-hipError_t by_dim(const AttentionGradParams &p, RowStats *stats, hipStream_t stream) {
-  if (p.dim <= 32) return run<T, 32, WAVES, BN>(p, stats, stream);
-  if (p.dim <= 64) return run<T, 64, WAVES, BN>(p, stats, stream);
-  if (p.dim <= 96) return run<T, 96, WAVES, BN>(p, stats, stream);
-  return run<T, 128, WAVES, BN>(p, stats, stream);
+hipError_t by_dim(const AttentionGradParams &p, float *ws, hipStream_t stream) {
+  if (p.dim <= 32) return run<T, 32, WAVES, BN>(p, ws, stream);
+  if (p.dim <= 64) return run<T, 64, WAVES, BN>(p, ws, stream);
+  if (p.dim <= 96) return run<T, 96, WAVES, BN>(p, ws, stream);
+  return run<T, 128, WAVES, BN>(p, ws, stream);
 }
 
 }  // namespace
 
 size_t attention_grad_workspace(int64_t tokens, int heads) {
-  return (size_t)tokens * heads * sizeof(RowStats);
+  return (size_t)tokens * heads * 2 * sizeof(float);
 }
 
-hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *ws,
+hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *workspace,
                                  hipStream_t stream) {
-  RowStats *stats = (RowStats *)ws;
+  float *ws = (float *)workspace;
   const bool few = (p.tokens > p.kv_tokens ? p.tokens : p.kv_tokens) / p.batch <= 48;
   if (dtype == kF32)
-    return few ? by_dim<F32, 1, 32>(p, stats, stream) : by_dim<F32, 4, 32>(p, stats, stream);
-  return few ? by_dim<BF16, 1, 32>(p, stats, stream) : by_dim<BF16, 4, 64>(p, stats, stream);
+    return few ? by_dim<F32, 1, 32>(p, ws, stream) : by_dim<F32, 4, 32>(p, ws, stream);
+  return few ? by_dim<BF16, 1, 32>(p, ws, stream) : by_dim<BF16, 4, 64>(p, ws, stream);
 }
 
 }  // namespace dlrm

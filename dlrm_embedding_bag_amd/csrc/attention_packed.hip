@@ -67,7 +67,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
-  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[L::SIZE], v1[L::SIZE];
+  constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
+  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
   __shared__ int found[WAVES];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -78,9 +79,9 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
   const float c = p.scale * kLog2e;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t tile = item / p.heads;
-    const int head = (int)(item - tile * p.heads);
-    const Tile t = find_tile(p.offsets, p.batch, p.tokens, tile, BM);
+    const Item at = item_of(item, tile_count(p.tokens, p.batch, BM), p.heads);
+    const int head = at.head;
+    const Tile t = find_tile(p.offsets, p.batch, p.tokens, at.tile, BM);
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // row of the tile
     if (t.sequence < 0) {
@@ -178,18 +179,27 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
       work(k, v, n);
     };
 
-    if (count > 0) fill(k0, v0, 0);
-    for (int n = 0; n < count; n += 2) {
-      landed();
-      if (n + 1 < count) fill(k1, v1, n + 1);
-      tile_of(k0, v0, n);
-      if (n + 1 < count) {
+    if constexpr (WAVES == 1) {
+      for (int n = 0; n < count; ++n) {
+        fill(k0, v0, n);
         landed();
-        if (n + 2 < count) fill(k0, v0, n + 2);
-        tile_of(k1, v1, n + 1);
+        tile_of(k0, v0, n);
+        landed();
       }
+    } else {
+      if (count > 0) fill(k0, v0, 0);
+      for (int n = 0; n < count; n += 2) {
+        landed();
+        if (n + 1 < count) fill(k1, v1, n + 1);
+        tile_of(k0, v0, n);
+        if (n + 1 < count) {
+          landed();
+          if (n + 2 < count) fill(k0, v0, n + 2);
+          tile_of(k1, v1, n + 1);
+        }
+      }
+      landed();  // nobody reads the tiles any more
     }
-    landed();  // nobody reads the tiles any more
 
     if (loose >= 0) {   // (weights are above zero, so the values add as they are)
       for (int j = loose * BN; j < seen.wave_any; ++j) {

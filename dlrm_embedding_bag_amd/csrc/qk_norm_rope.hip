@@ -282,24 +282,29 @@ __global__ __launch_bounds__(kThreads) void rope_grad_kernel(RopeParams p, int l
   if (p.k.dweight) put_weight_sums<N>(dk, s, p.dim, lanes, sums, to + p.dim);
 }
 
-// dweight[i] = the sum of the workgroups' shares, in 64 bits and a fixed order.
-__global__ __launch_bounds__(kThreads) void rope_weight_kernel(const float *partial, int blocks,
-                                                               int dim, float *dq, float *dk) {
-  __shared__ double part[kThreads / 16][16];
+// dweight[i] = the sum of the workgroups' shares, in 64 bits and a fixed order:
+// 16 elements a workgroup, its threads 64 shares at a time.
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void rope_weight_kernel(const float *partial, int blocks,
+                                                                  int dim, float *dq, float *dk) {
+  constexpr int GROUPS = kSumThreads / 16;
+  __shared__ double part[GROUPS][16];
   float *out = blockIdx.y ? dk : dq;
   if (!out) return;
-  const int i = blockIdx.x * 16 + (threadIdx.x & 15), g = threadIdx.x / 16;
+  const int e = threadIdx.x & 15, i = blockIdx.x * 16 + e, g = threadIdx.x / 16;
   double a = 0.0;
-  if (i < dim)
-    for (int b = g; b < blocks; b += kThreads / 16)
+  if (i < dim) {
+#pragma unroll 4
+    for (int b = g; b < blocks; b += GROUPS)
       a += (double)partial[((int64_t)b * 2 + blockIdx.y) * dim + i];
-  part[g][threadIdx.x & 15] = a;
-  __syncthreads();
-  if (threadIdx.x < 16 && i < dim) {
-    a = 0.0;
-    for (int j = 0; j < kThreads / 16; ++j) a += part[j][threadIdx.x];
-    out[i] = (float)a;
   }
+  part[g][e] = a;
+  __syncthreads();
+  for (int half = GROUPS / 2; half > 0; half /= 2) {
+    if (g < half) part[g][e] += part[g + half][e];
+    __syncthreads();
+  }
+  if (g == 0 && i < dim) out[i] = (float)part[0][e];
 }
 
 constexpr int kGradBlocks = 1024;   // four a CU
@@ -350,8 +355,8 @@ hipError_t run_backward(const RopeParams &p, int lanes, float *partial, hipStrea
                   lanes, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.q.dweight && !p.k.dweight)) return e;
-  launch_kernel(rope_weight_kernel, dim3((p.dim + 15) / 16, 2), dim3(kThreads), 0, stream,
-                (const float *)partial, blocks, p.dim, p.q.dweight, p.k.dweight);
+  launch_kernel(rope_weight_kernel, dim3((p.dim + 15) / 16, 2), dim3(kSumThreads), 0,
+                stream, (const float *)partial, blocks, p.dim, p.q.dweight, p.k.dweight);
   return hipGetLastError();
 }
 

@@ -88,20 +88,31 @@ __device__ __forceinline__ Operand<T> load_operand(const typename T::S *row, int
 }
 
 // ------------------------------------------------------------ tiles in LDS --
-// ROWS rows of DP elements as chunks of 16 bytes.  Chunk c of row r lies at
-// place c ^ (2 (r & 3) + (r >> 2 & 1)): eight rows read at one chunk start on
-// different banks, and so do two chunks each of four rows, which is what a
-// transposed read takes.
+// ROWS rows of DP elements as chunks of 16 bytes, C places a row.  LDS serves 256
+// bytes at once: 16 lanes of a row's read (16 rows, one chunk), 32 of a transposed
+// one (4 neighbouring rows, 4 neighbouring chunks), 64 of single floats (rows t and
+// t + 4, 8 neighbouring chunks).  So that none of these meet on a bank, chunk c of
+// row r lies at place c ^ key(r), where the places of 16 rows differ and
+//   bfloat16  four neighbouring rows differ in the key's upper two bits,
+//   float32   rows t and t + 4 in its uppermost.
+// (Of 64 keys and values in bfloat16 at dim 128 a read takes 4 cycles, or 2 if
+// transposed; with a three-bit key for eight rows 8 and 4.)
 template <typename T, int ROWS, int DP>
 struct LdsTile {
   using S = typename T::S;
   static constexpr int E = 16 / sizeof(S);                 // elements of a chunk
   static constexpr int C = DP == 96 ? 128 / E : DP / E;    // places of a row, a power of two
-  static constexpr int MASK = C < 8 ? C - 1 : 7;
   static constexpr int SIZE = ROWS * C;                    // chunks
+  static constexpr int BITS = C >= 16 ? 15 : C - 1;        // of a key
 
+  // of a row in 0 .. 15; keys repeat every 16 rows
   __device__ __forceinline__ static int key(int row) {
-    return ((row & 3) << 1 | (row >> 2 & 1)) & MASK;
+    if constexpr (E == 8)
+      return C >= 16  ? (row & 3) << 2 | (row >> 2 & 3)
+             : C == 8 ? (row & 2) << 1 | (row >> 2 & 3)     // two rows are 256 bytes
+                      : row >> 2 & 3;                       // four rows are
+    else
+      return C >= 16 ? (row & 4) << 1 | (row & 3) << 1 | (row >> 3 & 1) : row >> 1 & 7;
   }
 };
 
@@ -134,7 +145,7 @@ struct TileLoad {
   using L = LdsTile<T, ROWS, DP>;
   static constexpr int LOADS = L::SIZE / (WAVES * kWave);
   static constexpr int STEP = WAVES * kWave / L::C;   // rows of a load
-  static constexpr int KINDS = STEP % 8 ? LOADS : 1;  // keys repeat every eight rows
+  static constexpr int KINDS = STEP >= 16 ? 1 : LOADS * STEP < 16 ? LOADS : 16 / STEP;
   static_assert(L::SIZE % (WAVES * kWave) == 0 && WAVES * kWave % L::C == 0);
   static constexpr uint32_t kNowhere = 0x80000000u;   // beyond any tile: reads as zeros
   uint32_t from[KINDS];
@@ -143,7 +154,7 @@ struct TileLoad {
 #pragma unroll
     for (int i = 0; i < KINDS; ++i) {
       const int at = wave * kWave + lane, r = at / L::C;
-      const int c = ((at % L::C) ^ L::key(i * STEP + r)) * L::E;
+      const int c = ((at % L::C) ^ L::key((i * STEP + r) & 15)) * L::E;
       from[i] = c < dim ? (uint32_t)((r * row_stride + c) * (int64_t)sizeof(S)) : kNowhere;
     }
   }
@@ -157,15 +168,16 @@ struct TileLoad {
       const int left = n - i * STEP;
       const uint32_t bytes =
           left > 0 ? (uint32_t)((left - 1) * (uint32_t)row_stride + dim) * (uint32_t)sizeof(S) : 0;
-      load_to_lds(buffer_of(base + i * STEP * row_stride, bytes), from[KINDS == 1 ? 0 : i],
+      load_to_lds(buffer_of(base + i * STEP * row_stride, bytes), from[i % KINDS],
                   lds + (i * WAVES + wave) * kWave);
     }
   }
 };
 
-// What a lane reads of tiles: the places of its own row, or of its own columns,
-// at any of which the rest of an address is a constant.  (The key touches three
-// bits of a chunk's number, so few places serve all reads.)
+// What a lane reads of tiles: the place of its first chunk, or element.  Others
+// differ from it by an exclusive or with a constant, which takes a column and a
+// row's key along, and by whole rows.  here() keeps those exclusive ors where they
+// are used, for kernels that have no registers to hold them in.
 typedef const __attribute__((address_space(3))) char *LdsBytes;
 template <typename V>
 __device__ __forceinline__ V lds_at(const void *lds, uint32_t place) {
@@ -177,24 +189,21 @@ __device__ __forceinline__ V lds_at(const void *lds, uint32_t place) {
 template <typename T, int ROWS, int DP>
 struct ReadRows {
   using L = LdsTile<T, ROWS, DP>;
-  uint32_t place[4];
+  uint32_t place;
   __device__ __forceinline__ explicit ReadRows(int lane) {
-    const int r = lane & 31, h = lane >> 5;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = L::E == 8 ? i * 2 + h : (i >> 1) * 4 + h * 2 + (i & 1);
-      place[i] = (uint32_t)(r * L::C + ((c ^ L::key(r)) & (L::C - 1))) * 16;
-    }
+    const int r = lane & 31, c = (lane >> 5) * (8 / L::E);
+    place = (uint32_t)(r * L::C + (c ^ L::key(r & 15))) * 16;
   }
+  __device__ __forceinline__ void here() { asm volatile("" : "+v"(place)); }
   __device__ __forceinline__ Operand<T> read(const u32x4_t *lds, int r0, int step) const {
     Operand<T> o;
     if constexpr (L::E == 8) {
-      o.v = lds_at<u32x4_t>(lds, place[step & 3] + (r0 * L::C + (step >> 2) * 8) * 16);
+      o.v = lds_at<u32x4_t>(lds, (place ^ step * 32) + r0 * L::C * 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        o.v[e] = lds_at<f32x4_t>(
-            lds, place[(step & 1) * 2 + e] + (r0 * L::C + (step >> 1) * 8) * 16);
+      for (int e = 0; e < 2; ++e)   // 16 chunks are four steps
+        o.v[e] = lds_at<f32x4_t>(lds, (place ^ ((step & 3) * 4 + e) * 16) +
+                                          (r0 * L::C + step / 4 * 16) * 16);
     }
     return o;
   }
@@ -207,36 +216,37 @@ struct ReadRows {
 template <typename T, int ROWS, int DP>
 struct ReadColumns {
   using L = LdsTile<T, ROWS, DP>;
-  static constexpr int N = L::E == 8 ? 2 : 4;
-  uint32_t place[N];
+  uint32_t place;
   __device__ __forceinline__ explicit ReadColumns(int lane) {
     const int h = lane >> 5;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (L::E == 8) {
-        const int q = lane & 15, t = h * 4 + (q >> 2);
-        const int c = i * 4 + (lane >> 4 & 1) * 2 + (q >> 1 & 1);
-        place[i] = (uint32_t)(t * L::C + ((c ^ L::key(t)) & (L::C - 1))) * 16 + (q & 1) * 8;
-      } else {
-        const int t = h * 4 + i, c = (lane & 31) >> 2;
-        place[i] = (uint32_t)(t * L::C + (c ^ L::key(t))) * 16 + (lane & 3) * 4;
-      }
+    if constexpr (L::E == 8) {
+      const int q = lane & 15, t = h * 4 + (q >> 2), c = (lane >> 4 & 1) * 2 + (q >> 1 & 1);
+      place = (uint32_t)(t * L::C + (c ^ L::key(t))) * 16 + (q & 1) * 8;
+    } else {
+      const int t = h * 4, c = (lane & 31) >> 2;
+      place = (uint32_t)(t * L::C + (c ^ L::key(t))) * 16 + (lane & 3) * 4;
     }
   }
+  __device__ __forceinline__ void here() { asm volatile("" : "+v"(place)); }
   __device__ __forceinline__ Operand<T> read(const u32x4_t *lds, int r0, int d) const {
     Operand<T> o;
     if constexpr (L::E == 8) {
       typedef __attribute__((address_space(3))) i16x4_t *Quad;
-      const LdsBytes at = (LdsBytes)lds + (place[d & 1] + (r0 * L::C + (d >> 1) * 8) * 16);
-      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)at);
-      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)(at + 8 * L::C * 16));
+      const LdsBytes at = (LdsBytes)lds + r0 * L::C * 16;
+      const uint32_t by_key = (L::key(8) ^ d * 4) * 16;
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quad)(at + (place ^ d * 64)));
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (Quad)(at + ((place ^ by_key) + 8 * L::C * 16)));
       const auto a = __builtin_bit_cast(u32x2_u, lo), b = __builtin_bit_cast(u32x2_u, hi);
       o.v = u32x4_t{a[0], a[1], b[0], b[1]};
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 8; ++e) {
+        const int t = row_of(e, 0);                   // (rows t and t + 4 differ by a bit
+        const uint32_t by_key = (L::key(t) ^ (d & 1) * 8) * 16;  // that the place has)
         o.v[e >> 2][e & 3] = lds_at<float>(
-            lds, place[e & 3] + ((r0 + (e >> 2) * 8) * L::C + d * 8) * 16);
+            lds, (place ^ by_key) + ((r0 + t) * L::C + (L::C > 8 ? d / 2 * 16 : 0)) * 16);
+      }
     }
     return o;
   }

@@ -219,8 +219,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
   const TileLoad<T, BN, DP, WAVES> gload(wave, lane, p.grad.token, p.dim);
-  const ReadRows<T, BN, DP> by_row(lane);
-  const ReadColumns<T, BN, DP> by_column(lane);
+  ReadRows<T, BN, DP> by_row(lane);
+  ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
   const int32_t *key_offsets = p.kv_offsets ? p.kv_offsets : p.offsets;
   const Stats stats(ws, p.tokens, p.heads);
@@ -295,6 +295,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
       const bool masked = base < wave_full;
 #pragma unroll
       for (int j = 0; j < QT; ++j) {
+        by_row.here();
+        by_column.here();
         f32x16_t s = f32x16_t{}, dp;
 #pragma unroll
         for (int e = 0; e < STEPS; ++e) s = multiply(by_row.read(q, j * 32, e), k[e], s);

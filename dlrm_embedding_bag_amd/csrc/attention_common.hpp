@@ -260,6 +260,26 @@ __device__ __forceinline__ void landed() {
   asm volatile("" ::: "memory");
 }
 
+// N products in order, whose operands `read(i)` brings from LDS: each read stands
+// AHEAD products before its own, so that none waits for LDS.  PINNED: in just this
+// order (where nothing else is to do, the compiler saves registers and has each
+// product wait for its own read).
+template <typename T, int N, int AHEAD, bool PINNED, typename Read, typename Use>
+__device__ __forceinline__ void in_order(Read &&read, Use &&use) {
+  constexpr int A = AHEAD < N ? AHEAD : N;
+  Operand<T> a[A];
+#pragma unroll
+  for (int i = 0; i < A; ++i) a[i] = read(i);
+  if (PINNED) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Operand<T> now = a[i % A];
+    if (i + A < N) a[i % A] = read(i + A);
+    use(i, now);
+    if (PINNED) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // -------------------------------------------------------- packed sequences --
 // Sequence b of a packed batch holds rows offsets[b] .. offsets[b + 1] - 1.
 // With the rows before the first and behind the last these are batch + 2

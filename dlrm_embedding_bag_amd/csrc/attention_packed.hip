@@ -67,6 +67,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
+  constexpr int AHEAD = sizeof(S) == 2 ? 4 : 2;
   constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
   __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
   __shared__ int found[WAVES];
@@ -126,12 +127,12 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
       const bool masked = seen.wave_all - base < BN;
       f32x16_t s[KT];
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        s[j] = f32x16_t{};
-#pragma unroll
-        for (int e = 0; e < STEPS; ++e)
-          s[j] = multiply(by_row.read(k, j * 32, e), q[e], s[j]);
-      }
+      for (int j = 0; j < KT; ++j) s[j] = f32x16_t{};
+      in_order<T, KT * STEPS, AHEAD, true>(
+          [&](int i) { return by_row.read(k, i / STEPS * 32, i % STEPS); },
+          [&](int i, const Operand<T> &a) {
+            s[i / STEPS] = multiply(a, q[i % STEPS], s[i / STEPS]);
+          });
       if (masked) {
         const int left = seen.mine - base;
 #pragma unroll
@@ -156,19 +157,26 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
         m = next;
       }
       const float from = m == -INFINITY ? 0.0f : m;
+      // the weights of 16 keys at a time, those of the next 16 between the products
+      auto weigh = [&](int i) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16], c, -from));
+        s[i / 16][i % 16] = x;
+        l += x;
+      };
 #pragma unroll
-      for (int j = 0; j < KT; ++j)
+      for (int i = 0; i < 8; ++i) weigh(i);
+      Operand<T> w;
+      in_order<T, BN / 16 * DT, AHEAD, false>(
+          [&](int i) { return by_column.read(v, i / DT * 16, i % DT); },
+          [&](int i, const Operand<T> &a) {
+            const int j = i / DT, d = i % DT;
+            if (d == 0) w = operand_of<T>(s[j / 2], j % 2);
+            o[d] = multiply(a, w, o[d]);
+            if (j + 1 < BN / 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -from));
-          l += s[j][i];
-        }
-#pragma unroll
-      for (int j = 0; j < BN / 16; ++j) {
-        const Operand<T> w = operand_of<T>(s[j >> 1], j & 1);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] = multiply(by_column.read(v, j * 16, d), w, o[d]);
-      }
+              for (int e = d * 8 / DT; e < (d + 1) * 8 / DT; ++e) weigh(8 * (j + 1) + e);
+            }
+          });
     };
     // A value that is not finite must not reach the rows that do not see it, and
     // zero times it is not zero: from the first tile on that some row does not see

@@ -116,6 +116,11 @@ struct LdsTile {
   }
 };
 
+// Tiles are passed by their addresses in LDS.
+typedef __attribute__((address_space(3))) u32x4_t *LdsChunks;
+typedef __attribute__((address_space(3))) float *LdsFloats;
+typedef const __attribute__((address_space(3))) char *LdsBytes;
+
 // `bytes` of memory from `base` on, behind which loads read zeros.  (These two
 // are no templates: the host's pass drops kernels whose templates call such
 // builtins twice.)
@@ -124,10 +129,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, ui
 }
 // 16 or 4 bytes a lane, from memory to LDS: lane l's to lds[l].
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t from,
-                                            u32x4_t *lds) {
+                                            LdsChunks lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds, 16, from, 0, 0, 0);
 }
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t from, float *lds) {
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t from, LdsFloats lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds, 4, from, 0, 0, 0);
 }
 
@@ -137,40 +142,45 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
 }
 
-// What a thread asks for when a tile is filled: where its chunks lie in memory,
-// relative to the first row of each load.
+// Fills tiles one after another with the rows of a tensor: a wave's loads keep
+// their lanes' offsets, and only the buffer moves on (10 scalar instructions a tile;
+// with a buffer for each load there were 80, a sixth of the kernel's time).
 template <typename T, int ROWS, int DP, int WAVES>
 struct TileLoad {
   using S = typename T::S;
   using L = LdsTile<T, ROWS, DP>;
   static constexpr int LOADS = L::SIZE / (WAVES * kWave);
-  static constexpr int STEP = WAVES * kWave / L::C;   // rows of a load
-  static constexpr int KINDS = STEP >= 16 ? 1 : LOADS * STEP < 16 ? LOADS : 16 / STEP;
   static_assert(L::SIZE % (WAVES * kWave) == 0 && WAVES * kWave % L::C == 0);
   static constexpr uint32_t kNowhere = 0x80000000u;   // beyond any tile: reads as zeros
-  uint32_t from[KINDS];
+  uint32_t from[LOADS];
+  const S *next;        // the first row of the next tile
+  int left;             // rows from there on (what lies behind becomes zeros)
+  int64_t step;         // elements of a tile's rows
+  uint32_t row_bytes, last_bytes;
 
   __device__ __forceinline__ TileLoad(int wave, int lane, int64_t row_stride, int dim) {
 #pragma unroll
-    for (int i = 0; i < KINDS; ++i) {
-      const int at = wave * kWave + lane, r = at / L::C;
-      const int c = ((at % L::C) ^ L::key((i * STEP + r) & 15)) * L::E;
+    for (int i = 0; i < LOADS; ++i) {
+      const int at = (i * WAVES + wave) * kWave + lane, r = at / L::C;
+      const int c = ((at % L::C) ^ L::key(r & 15)) * L::E;
       from[i] = c < dim ? (uint32_t)((r * row_stride + c) * (int64_t)sizeof(S)) : kNowhere;
     }
+    step = row_stride * ROWS;
+    row_bytes = (uint32_t)row_stride * (uint32_t)sizeof(S);
+    last_bytes = (uint32_t)dim * (uint32_t)sizeof(S);
   }
-  // Rows `base` on, of which `rows` are there (the others become zeros); the
-  // loads are on their way when this returns.
-  __device__ __forceinline__ void fill(u32x4_t *lds, const S *base, int rows, int64_t row_stride,
-                                       int dim, int wave) const {
-    const int n = rows < ROWS ? rows : ROWS;
+  __device__ __forceinline__ void start(const S *base, int rows) {
+    next = base;
+    left = rows;
+  }
+  // The loads are on their way when this returns.
+  __device__ __forceinline__ void fill(LdsChunks lds, int wave) {
+    const uint32_t rows = left < ROWS ? left : ROWS;
+    const auto b = buffer_of(next, (rows - 1) * row_bytes + last_bytes);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int left = n - i * STEP;
-      const uint32_t bytes =
-          left > 0 ? (uint32_t)((left - 1) * (uint32_t)row_stride + dim) * (uint32_t)sizeof(S) : 0;
-      load_to_lds(buffer_of(base + i * STEP * row_stride, bytes), from[i % KINDS],
-                  lds + (i * WAVES + wave) * kWave);
-    }
+    for (int i = 0; i < LOADS; ++i) load_to_lds(b, from[i], lds + (i * WAVES + wave) * kWave);
+    next += step;
+    left -= ROWS;
   }
 };
 
@@ -178,10 +188,9 @@ struct TileLoad {
 // differ from it by an exclusive or with a constant, which takes a column and a
 // row's key along, and by whole rows.  here() keeps those exclusive ors where they
 // are used, for kernels that have no registers to hold them in.
-typedef const __attribute__((address_space(3))) char *LdsBytes;
 template <typename V>
-__device__ __forceinline__ V lds_at(const void *lds, uint32_t place) {
-  return *(const __attribute__((address_space(3))) V *)((LdsBytes)lds + place);
+__device__ __forceinline__ V lds_at(LdsBytes lds, uint32_t place) {
+  return *(const __attribute__((address_space(3))) V *)(lds + place);
 }
 
 // Row r0 + lane % 32 of a tile, elements 16 step + 8 (lane / 32) on: the operand
@@ -195,14 +204,14 @@ struct ReadRows {
     place = (uint32_t)(r * L::C + (c ^ L::key(r & 15))) * 16;
   }
   __device__ __forceinline__ void here() { asm volatile("" : "+v"(place)); }
-  __device__ __forceinline__ Operand<T> read(const u32x4_t *lds, int r0, int step) const {
+  __device__ __forceinline__ Operand<T> read(LdsChunks lds, int r0, int step) const {
     Operand<T> o;
     if constexpr (L::E == 8) {
-      o.v = lds_at<u32x4_t>(lds, (place ^ step * 32) + r0 * L::C * 16);
+      o.v = lds_at<u32x4_t>((LdsBytes)lds, (place ^ step * 32) + r0 * L::C * 16);
     } else {
 #pragma unroll
       for (int e = 0; e < 2; ++e)   // 16 chunks are four steps
-        o.v[e] = lds_at<f32x4_t>(lds, (place ^ ((step & 3) * 4 + e) * 16) +
+        o.v[e] = lds_at<f32x4_t>((LdsBytes)lds, (place ^ ((step & 3) * 4 + e) * 16) +
                                           (r0 * L::C + step / 4 * 16) * 16);
     }
     return o;
@@ -228,7 +237,7 @@ struct ReadColumns {
     }
   }
   __device__ __forceinline__ void here() { asm volatile("" : "+v"(place)); }
-  __device__ __forceinline__ Operand<T> read(const u32x4_t *lds, int r0, int d) const {
+  __device__ __forceinline__ Operand<T> read(LdsChunks lds, int r0, int d) const {
     Operand<T> o;
     if constexpr (L::E == 8) {
       typedef __attribute__((address_space(3))) i16x4_t *Quad;
@@ -245,7 +254,7 @@ struct ReadColumns {
         const int t = row_of(e, 0);                   // (rows t and t + 4 differ by a bit
         const uint32_t by_key = (L::key(t) ^ (d & 1) * 8) * 16;  // that the place has)
         o.v[e >> 2][e & 3] = lds_at<float>(
-            lds, (place ^ by_key) + ((r0 + t) * L::C + (L::C > 8 ? d / 2 * 16 : 0)) * 16);
+            (LdsBytes)lds, (place ^ by_key) + ((r0 + t) * L::C + (L::C > 8 ? d / 2 * 16 : 0)) * 16);
       }
     }
     return o;

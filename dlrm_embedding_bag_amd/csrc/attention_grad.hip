@@ -75,8 +75,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
   __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
-  const TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
+  TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
+  TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
   const ReadRows<T, BN, DP> by_row(lane);
   const ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
@@ -101,8 +101,6 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
     const SeenKeys seen(p.causal != 0, keys.count, t.left, BM, wave, lane);
     const int count = seen.tile_any / BN + (seen.tile_any % BN != 0);
     const int kv_head = head / p.group;
-    const S *kbase = (const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head;
-    const S *vbase = (const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head;
 
     Operand<T> q[STEPS], g[STEPS];
     float delta = 0.0f;
@@ -130,13 +128,13 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
     f32x16_t o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
-    auto fill = [&](u32x4_t *k, u32x4_t *v, int n) {
-      kload.fill(k, kbase + (int64_t)n * BN * p.k.token, keys.count - n * BN, p.k.token, p.dim,
-                 wave);
-      vload.fill(v, vbase + (int64_t)n * BN * p.v.token, keys.count - n * BN, p.v.token, p.dim,
-                 wave);
+    kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
+    vload.start((const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head, keys.count);
+    auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
+      kload.fill(k, wave);
+      vload.fill(v, wave);
     };
-    auto work = [&](const u32x4_t *k, const u32x4_t *v, int n) {
+    auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       const int base = n * BN;
       if (base >= seen.wave_any) return;
       const bool masked = seen.wave_all - base < BN;
@@ -168,21 +166,21 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
     };
     if constexpr (WAVES == 1) {
       for (int n = 0; n < count; ++n) {
-        fill(k0, v0, n);
+        fill((LdsChunks)k0, (LdsChunks)v0);
         landed();
-        work(k0, v0, n);
+        work((LdsChunks)k0, (LdsChunks)v0, n);
         landed();
       }
     } else {
-      if (count > 0) fill(k0, v0, 0);
+      if (count > 0) fill((LdsChunks)k0, (LdsChunks)v0);
       for (int n = 0; n < count; n += 2) {
         landed();
-        if (n + 1 < count) fill(k1, v1, n + 1);
-        work(k0, v0, n);
+        if (n + 1 < count) fill((LdsChunks)k1, (LdsChunks)v1);
+        work((LdsChunks)k0, (LdsChunks)v0, n);
         if (n + 1 < count) {
           landed();
-          if (n + 2 < count) fill(k0, v0, n + 2);
-          work(k1, v1, n + 1);
+          if (n + 2 < count) fill((LdsChunks)k0, (LdsChunks)v0);
+          work((LdsChunks)k1, (LdsChunks)v1, n + 1);
         }
       }
       landed();
@@ -196,7 +194,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
 // The statistics of a tile's rows, 64 a load; behind the last row zeros (whose
 // gradient is zero, too, so they add nothing).
 template <int BN, int WAVES>
-__device__ __forceinline__ void fill_stats(float *lds, const Stats &stats, int64_t at, int rows,
+__device__ __forceinline__ void fill_stats(LdsFloats lds, const Stats &stats, int64_t at, int rows,
                                            int wave, int lane) {
   static_assert(BN <= kWave);
   const int n = rows < BN ? rows : BN;
@@ -217,8 +215,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
   __shared__ float s0[2 * kWave], s1[2 * kWave];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
-  const TileLoad<T, BN, DP, WAVES> gload(wave, lane, p.grad.token, p.dim);
+  TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
+  TileLoad<T, BN, DP, WAVES> gload(wave, lane, p.grad.token, p.dim);
   ReadRows<T, BN, DP> by_row(lane);
   ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
@@ -275,21 +273,26 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
         v[s] = load_operand<T>(vat, s * 16 + half * 8, p.dim, there);
       }
     }
+    int64_t stat = 0;   // of the next tile's first row
     f32x16_t ok[DT], ov[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) ok[d] = ov[d] = f32x16_t{};
 
     // tiles of rows, head by head of the group
-    auto fill = [&](u32x4_t *q, u32x4_t *g, float *st, int h, int n) {
-      const int64_t head = (int64_t)kv_head * p.group + h, row = rows.first + (int64_t)n * BN;
-      const int left = rows.count - n * BN;
-      qload.fill(q, (const S *)p.q.data + row * p.q.token + head * p.q.head, left, p.q.token,
-                 p.dim, wave);
-      gload.fill(g, (const S *)p.grad.data + row * p.grad.token + head * p.grad.head, left,
-                 p.grad.token, p.dim, wave);
-      fill_stats<BN, WAVES>(st, stats, head * p.tokens + row, left, wave, lane);
+    auto start = [&](int h) __attribute__((always_inline)) {
+      const int64_t head = (int64_t)kv_head * p.group + h, row = rows.first + (int64_t)n0 * BN;
+      qload.start((const S *)p.q.data + row * p.q.token + head * p.q.head, rows.count - n0 * BN);
+      gload.start((const S *)p.grad.data + row * p.grad.token + head * p.grad.head,
+                  rows.count - n0 * BN);
+      stat = head * p.tokens + row;
     };
-    auto work = [&](const u32x4_t *q, const u32x4_t *g, const float *st, int n) {
+    auto fill = [&](LdsChunks q, LdsChunks g, LdsFloats st) __attribute__((always_inline)) {
+      fill_stats<BN, WAVES>(st, stats, stat, qload.left, wave, lane);
+      qload.fill(q, wave);
+      gload.fill(g, wave);
+      stat += BN;
+    };
+    auto work = [&](LdsChunks q, LdsChunks g, LdsFloats st, int n) __attribute__((always_inline)) {
       const int base = n * BN;
       if (wave_from - base >= BN) return;
       const bool masked = base < wave_full;
@@ -302,8 +305,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
         for (int e = 0; e < STEPS; ++e) s = multiply(by_row.read(q, j * 32, e), k[e], s);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const f32x4_t lse2 = lds_at<f32x4_t>(st, by_stat + (j * 32 + i * 2) * 4);
-          const f32x4_t from = lds_at<f32x4_t>(st, by_stat + (kWave + j * 32 + i * 2) * 4);
+          const f32x4_t lse2 = lds_at<f32x4_t>((LdsBytes)st, by_stat + (j * 32 + i * 2) * 4);
+          const f32x4_t from = lds_at<f32x4_t>((LdsBytes)st, by_stat + (kWave + j * 32 + i * 2) * 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -lse2[e]));
@@ -331,43 +334,30 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
         }
       }
     };
-    int h = 0, n = n0;            // the tile that is worked on
-    int fh = 0, fn = n0;          // the tile that is asked for next
-    auto next = [&](int &hh, int &nn) {
-      if (++nn == n0 + per_head) nn = n0, ++hh;
-    };
-    const int heads = per_head > 0 ? p.group : 0;
-    if constexpr (WAVES == 1) {
-      while (h < heads) {
-        fill(q0, g0, s0, h, n);
-        landed();
-        work(q0, g0, s0, n);
-        landed();
-        next(h, n);
-      }
-    } else {
-      if (heads) {
-        fill(q0, g0, s0, fh, fn);
-        next(fh, fn);
-      }
-      while (h < heads) {
-        landed();
-        if (fh < heads) {
-          fill(q1, g1, s1, fh, fn);
-          next(fh, fn);
+    for (int h = 0; h < p.group; ++h) {
+      if (per_head <= 0) break;
+      start(h);
+      if constexpr (WAVES == 1) {
+        for (int n = 0; n < per_head; ++n) {
+          fill((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0);
+          landed();
+          work((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0, n0 + n);
+          landed();
         }
-        work(q0, g0, s0, n);
-        next(h, n);
-        if (h >= heads) break;
-        landed();
-        if (fh < heads) {
-          fill(q0, g0, s0, fh, fn);
-          next(fh, fn);
+      } else {
+        fill((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0);
+        for (int n = 0; n < per_head; n += 2) {
+          landed();
+          if (n + 1 < per_head) fill((LdsChunks)q1, (LdsChunks)g1, (LdsFloats)s1);
+          work((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0, n0 + n);
+          if (n + 1 < per_head) {
+            landed();
+            if (n + 2 < per_head) fill((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0);
+            work((LdsChunks)q1, (LdsChunks)g1, (LdsFloats)s1, n0 + n + 1);
+          }
         }
-        work(q1, g1, s1, n);
-        next(h, n);
+        landed();
       }
-      landed();
     }
     if (mine < t.left) {
       const int64_t key = (int64_t)t.row + mine;

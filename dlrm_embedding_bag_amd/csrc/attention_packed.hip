@@ -30,7 +30,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 // A tile of values in LDS: whether it holds one that is not finite, for all
 // waves; if so it is zero there when this returns.
 template <typename T, int SIZE, int WAVES>
-__device__ __forceinline__ bool clean(u32x4_t *v, int *found, int wave, int lane) {
+__device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int lane) {
   constexpr int EACH = SIZE / (WAVES * kWave);
   uint32_t others = 0;
 #pragma unroll
@@ -47,7 +47,7 @@ __device__ __forceinline__ bool clean(u32x4_t *v, int *found, int wave, int lane
   for (int w = 0; w < WAVES; ++w) any |= found[w] != 0;
   if (!uniform((int)any)) return false;
   for (int i = 0; i < EACH; ++i) {
-    u32x4_t *at = v + (i * WAVES + wave) * kWave + lane;
+    LdsChunks at = v + (i * WAVES + wave) * kWave + lane;
     u32x4_t w = *at;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -73,8 +73,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
   __shared__ int found[WAVES];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
-  const TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
+  TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
+  TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
   const ReadRows<T, BN, DP> by_row(lane);
   const ReadColumns<T, BN, DP> by_column(lane);
   const float c = p.scale * kLog2e;
@@ -100,7 +100,6 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     const SeenKeys seen(p.causal != 0, keys.count, t.left, BM, wave, lane);
     const int count = seen.tile_any / BN + (seen.tile_any % BN != 0);
     const int kv_head = head / p.group;
-    const S *kbase = (const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head;
     const S *vbase = (const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head;
     Operand<T> q[STEPS];
     {
@@ -115,13 +114,13 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     float m = -INFINITY, l = 0.0f;
     int loose = -1;   // the first tile whose values are not all added
 
-    auto fill = [&](u32x4_t *k, u32x4_t *v, int n) {
-      kload.fill(k, kbase + (int64_t)n * BN * p.k.token, keys.count - n * BN, p.k.token, p.dim,
-                 wave);
-      vload.fill(v, vbase + (int64_t)n * BN * p.v.token, keys.count - n * BN, p.v.token, p.dim,
-                 wave);
+    kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
+    vload.start(vbase, keys.count);
+    auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
+      kload.fill(k, wave);
+      vload.fill(v, wave);
     };
-    auto work = [&](const u32x4_t *k, const u32x4_t *v, int n) {
+    auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       const int base = n * BN;
       if (base >= seen.wave_any) return;
       const bool masked = seen.wave_all - base < BN;
@@ -129,10 +128,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
 #pragma unroll
       for (int j = 0; j < KT; ++j) s[j] = f32x16_t{};
       in_order<T, KT * STEPS, AHEAD, true>(
-          [&](int i) { return by_row.read(k, i / STEPS * 32, i % STEPS); },
-          [&](int i, const Operand<T> &a) {
-            s[i / STEPS] = multiply(a, q[i % STEPS], s[i / STEPS]);
-          });
+          [&](int i) { return by_row.read(k, i % KT * 32, i / KT); },
+          [&](int i, const Operand<T> &a) { s[i % KT] = multiply(a, q[i / KT], s[i % KT]); });
       if (masked) {
         const int left = seen.mine - base;
 #pragma unroll
@@ -158,7 +155,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
       }
       const float from = m == -INFINITY ? 0.0f : m;
       // the weights of 16 keys at a time, those of the next 16 between the products
-      auto weigh = [&](int i) {
+      auto weigh = [&](int i) __attribute__((always_inline)) {
         const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 16][i % 16], c, -from));
         s[i / 16][i % 16] = x;
         l += x;
@@ -181,7 +178,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     // A value that is not finite must not reach the rows that do not see it, and
     // zero times it is not zero: from the first tile on that some row does not see
     // whole, such values are left out, and added after the last tile.
-    auto tile_of = [&](const u32x4_t *k, u32x4_t *v, int n) {
+    auto tile_of = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       if (p.causal && seen.tile_all - n * BN < BN && clean<T, L::SIZE, WAVES>(v, found, wave, lane))
         loose = loose < 0 ? n : loose;
       work(k, v, n);
@@ -189,21 +186,21 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
 
     if constexpr (WAVES == 1) {
       for (int n = 0; n < count; ++n) {
-        fill(k0, v0, n);
+        fill((LdsChunks)k0, (LdsChunks)v0);
         landed();
-        tile_of(k0, v0, n);
+        tile_of((LdsChunks)k0, (LdsChunks)v0, n);
         landed();
       }
     } else {
-      if (count > 0) fill(k0, v0, 0);
+      if (count > 0) fill((LdsChunks)k0, (LdsChunks)v0);
       for (int n = 0; n < count; n += 2) {
         landed();
-        if (n + 1 < count) fill(k1, v1, n + 1);
-        tile_of(k0, v0, n);
+        if (n + 1 < count) fill((LdsChunks)k1, (LdsChunks)v1);
+        tile_of((LdsChunks)k0, (LdsChunks)v0, n);
         if (n + 1 < count) {
           landed();
-          if (n + 2 < count) fill(k0, v0, n + 2);
-          tile_of(k1, v1, n + 1);
+          if (n + 2 < count) fill((LdsChunks)k0, (LdsChunks)v0);
+          tile_of((LdsChunks)k1, (LdsChunks)v1, n + 1);
         }
       }
       landed();  // nobody reads the tiles any more

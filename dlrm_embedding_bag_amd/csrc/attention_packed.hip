@@ -20,6 +20,11 @@
 namespace dlrm {
 namespace {
 
+// The running maximum is a reference for the exponentials, which may exceed 1: it
+// follows a larger score only where that lies 2^kSlack above it, so that sums and
+// outputs are seldom scaled (at every tile of most rows otherwise).
+constexpr float kSlack = 8.0f;
+
 // Sign bits of a word's elements that are not finite.
 template <typename T>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -145,13 +150,14 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[j][i]);
       top = fmaxf(top, __uint_as_float(lane_xor<32>(__float_as_uint(top))));
       const float next = fmaxf(m, top * c);
-      if (__any(next > m)) {
+      if (__any(next > m + kSlack)) {
         // (a row that has seen nothing has m -inf and nothing to scale)
-        const float back = next > m ? __builtin_amdgcn_exp2f(m - next) : 1.0f;
+        const bool mine = next > m + kSlack;   // (a row does not follow another's)
+        const float back = mine ? __builtin_amdgcn_exp2f(m - next) : 1.0f;
         l *= back;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= back;
-        m = next;
+        m = mine ? next : m;
       }
       const float from = m == -INFINITY ? 0.0f : m;
       // the weights of 16 keys at a time, those of the next 16 between the products

@@ -261,6 +261,11 @@ struct ReadColumns {
   }
 };
 
+// Waves of a SIMD that a kernel leaves registers for: two cover each other's waits,
+// but float32 rows of more than 64 would spill (XX).
+template <typename T, int DP>
+constexpr int waves_a_simd = sizeof(typename T::S) == 4 && DP > 64 ? 1 : 2;
+
 // Loads to LDS and LDS accesses of this wave are done, and everyone's.
 __device__ __forceinline__ void landed() {
   __builtin_amdgcn_s_waitcnt(0x0070);
@@ -357,26 +362,27 @@ __device__ __forceinline__ Range rows_of(const int32_t *offsets, int64_t batch, 
 }
 
 // How many keys, from the first on, are seen: all, or with `causal` by the last
-// row all and by each row before it one less.  Rows count from the tile's first.
+// row all and by each row before it one less.  Rows count from the tile's first,
+// of which the tile has `tile_rows`, this wave `wave_rows`.
 struct SeenKeys {
-  int wave_all;  // by every row of the wave's 32 (that is there)
+  int causal, keys, left;
+  int wave_all;  // by every row of the wave (that is there)
   int wave_any;  // by any of them
   int tile_all;  // by every row of the workgroup's tile
   int tile_any;  // by any of them
-  int mine;      // by this lane's row
-  __device__ __forceinline__ SeenKeys(bool causal, int keys, int rows_left, int tile_rows, int wave,
-                                      int lane) {
-    auto by = [&](int r) {
-      const int n = causal ? keys - (rows_left - 1 - r) : keys;
-      return n < 0 ? 0 : n;
-    };
-    auto end = [&](int r) { return r < rows_left - 1 ? r : rows_left - 1; };
-    const int first = wave * 32, row = first + (lane & 31);
-    mine = row < rows_left ? by(row) : 0;
-    wave_all = first < rows_left ? by(first) : 0;
-    wave_any = first < rows_left ? by(end(first + 31)) : 0;
+  __device__ __forceinline__ SeenKeys(int causal_, int keys_, int rows_left, int tile_rows,
+                                      int wave, int wave_rows)
+      : causal(causal_), keys(keys_), left(rows_left) {
+    const int first = wave * wave_rows;
+    wave_all = by(first);
+    wave_any = first < left ? by(end(first + wave_rows - 1)) : 0;
     tile_all = by(0);
     tile_any = by(end(tile_rows - 1));
+  }
+  __device__ __forceinline__ int end(int r) const { return r < left - 1 ? r : left - 1; }
+  __device__ __forceinline__ int by(int r) const {   // 0 for a row that is not there
+    const int n = causal ? keys - (left - 1 - r) : keys;
+    return n < 0 || r >= left ? 0 : n;
   }
 };
 

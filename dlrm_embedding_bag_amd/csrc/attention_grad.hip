@@ -66,11 +66,12 @@ __device__ __forceinline__ float dot(const Operand<T> &a, const Operand<T> &b, f
 
 // Rows: dq, and the rows' statistics.
 template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGradParams p,
+__global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows_kernel(AttentionGradParams p,
                                                                  float *ws, int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
+  constexpr int AHEAD = sizeof(S) == 2 ? 4 : 2;
   constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
   __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
@@ -98,7 +99,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
     }
     const Range keys = p.kv_offsets ? rows_of(p.kv_offsets, p.batch, p.kv_tokens, t.sequence)
                                     : Range{t.first, t.row - t.first + t.left};
-    const SeenKeys seen(p.causal != 0, keys.count, t.left, BM, wave, lane);
+    const SeenKeys seen(p.causal, keys.count, t.left, BM, wave, 32);
+    const int seen_keys = seen.by(mine);
     const int count = seen.tile_any / BN + (seen.tile_any % BN != 0);
     const int kv_head = head / p.group;
 
@@ -138,15 +140,18 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
       const int base = n * BN;
       if (base >= seen.wave_any) return;
       const bool masked = seen.wave_all - base < BN;
-      const int left = seen.mine - base;
+      const int left = seen_keys - base;
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
         f32x16_t s = f32x16_t{}, dp = f32x16_t{};
-#pragma unroll
-        for (int e = 0; e < STEPS; ++e) {
-          s = multiply(by_row.read(k, j * 32, e), q[e], s);
-          dp = multiply(by_row.read(v, j * 32, e), g[e], dp);
-        }
+        in_order<T, 2 * STEPS, AHEAD, true>(
+            [&](int i) { return by_row.read(i % 2 ? v : k, j * 32, i / 2); },
+            [&](int i, const Operand<T> &a) {
+              if (i % 2)
+                dp = multiply(a, g[i / 2], dp);
+              else
+                s = multiply(a, q[i / 2], s);
+            });
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
@@ -155,13 +160,10 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_rows_kernel(AttentionGra
           for (int i = 0; i < 16; ++i)
             if (j * 32 + row_of(i, half) >= left) s[i] = 0.0f;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const Operand<T> w = operand_of<T>(s, h);
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            o[d] = multiply(by_column.read(k, j * 32 + h * 16, d), w, o[d]);
-        }
+        const Operand<T> w[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
+        in_order<T, 2 * DT, AHEAD, true>(
+            [&](int i) { return by_column.read(k, j * 32 + i / DT * 16, i % DT); },
+            [&](int i, const Operand<T> &a) { o[i % DT] = multiply(a, w[i / DT], o[i % DT]); });
       }
     };
     if constexpr (WAVES == 1) {
@@ -204,12 +206,13 @@ __device__ __forceinline__ void fill_stats(LdsFloats lds, const Stats &stats, in
 
 // Keys: dk and dv.  A lane holds one key of its wave's 32.
 template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGradParams p,
+__global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys_kernel(AttentionGradParams p,
                                                                  float *ws, int kv_heads,
                                                                  int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, QT = BN / 32, STEPS = DP / 16, DT = DP / 32;
+  constexpr int AHEAD = 1;
   constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
   __shared__ u32x4_t q0[L::SIZE], g0[L::SIZE], q1[SECOND], g1[SECOND];
   __shared__ float s0[2 * kWave], s1[2 * kWave];
@@ -301,8 +304,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
         by_row.here();
         by_column.here();
         f32x16_t s = f32x16_t{}, dp;
-#pragma unroll
-        for (int e = 0; e < STEPS; ++e) s = multiply(by_row.read(q, j * 32, e), k[e], s);
+        in_order<T, STEPS, AHEAD, false>([&](int i) { return by_row.read(q, j * 32, i); },
+                                        [&](int i, const Operand<T> &a) { s = multiply(a, k[i], s); });
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const f32x4_t lse2 = lds_at<f32x4_t>((LdsBytes)st, by_stat + (j * 32 + i * 2) * 4);
@@ -313,8 +316,9 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
             dp[i + e] = from[e];
           }
         }
-#pragma unroll
-        for (int e = 0; e < STEPS; ++e) dp = multiply(by_row.read(g, j * 32, e), v[e], dp);
+        in_order<T, STEPS, AHEAD, false>(
+            [&](int i) { return by_row.read(g, j * 32, i); },
+            [&](int i, const Operand<T> &a) { dp = multiply(a, v[i], dp); });
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] *= s[i];
         if (masked) {
@@ -323,15 +327,17 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void grad_keys_kernel(AttentionGra
           for (int i = 0; i < 16; ++i)
             if (j * 32 + row_of(i, half) < from) s[i] = dp[i] = 0.0f;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const Operand<T> wp = operand_of<T>(s, h), wd = operand_of<T>(dp, h);
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            ov[d] = multiply(by_column.read(g, j * 32 + h * 16, d), wp, ov[d]);
-            ok[d] = multiply(by_column.read(q, j * 32 + h * 16, d), wd, ok[d]);
-          }
-        }
+        const Operand<T> wp[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
+        const Operand<T> wd[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
+        in_order<T, 4 * DT, AHEAD, false>(
+            [&](int i) { return by_column.read(i % 2 ? q : g, j * 32 + i / 2 / DT * 16, i / 2 % DT); },
+            [&](int i, const Operand<T> &a) {
+              const int h = i / 2 / DT, d = i / 2 % DT;
+              if (i % 2)
+                ok[d] = multiply(a, wd[h], ok[d]);
+              else
+                ov[d] = multiply(a, wp[h], ov[d]);
+            });
       }
     };
     for (int h = 0; h < p.group; ++h) {

@@ -15,56 +15,10 @@
 // SIMD cover each other.
 #include <math.h>
 
-#include "attention_common.hpp"
+#include "attention_forward.hpp"
 
 namespace dlrm {
 namespace {
-
-// The running maximum is a reference for the exponentials, which may exceed 1: it
-// follows a larger score only where that lies 2^kSlack above it, so that sums and
-// outputs are seldom scaled (at every tile of most rows otherwise).
-constexpr float kSlack = 8.0f;
-
-// Sign bits of a word's elements that are not finite.
-template <typename T>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  return sizeof(typename T::S) == 4 ? ((w & 0x7fffffffu) + 0x00800000u) & 0x80000000u
-                                    : ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
-}
-
-// A tile of values in LDS: whether it holds one that is not finite, for all
-// waves; if so it is zero there when this returns.
-template <typename T, int SIZE, int WAVES>
-__device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int lane) {
-  constexpr int EACH = SIZE / (WAVES * kWave);
-  uint32_t others = 0;
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) {
-    const u32x4_t w = v[(i * WAVES + wave) * kWave + lane];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) others |= not_finite<T>(w[e]);
-  }
-  const bool mine = __any(others != 0);
-  if (lane == 0) found[wave] = mine;
-  landed();
-  bool any = false;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) any |= found[w] != 0;
-  if (!uniform((int)any)) return false;
-  for (int i = 0; i < EACH; ++i) {
-    LdsChunks at = v + (i * WAVES + wave) * kWave + lane;
-    u32x4_t w = *at;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t n = not_finite<T>(w[e]);
-      // a sign bit to all bits of its element
-      w[e] &= ~(sizeof(typename T::S) == 4 ? (n ? 0xffffffffu : 0u) : (n >> 15) * 0xffffu);
-    }
-    *at = w;
-  }
-  landed();
-  return true;
-}
 
 template <typename T, int DP, int WAVES, int BN>
 __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionParams p,
@@ -91,18 +45,13 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // row of the tile
     if (t.sequence < 0) {
-      const int64_t row = (int64_t)t.row + mine;
-      if (mine < t.left && half == 0) {
-        S *out = (S *)p.out.data + row * p.out.token + head * p.out.head;
-        if (p.fill & 1)
-          for (int d = 0; d < p.dim; ++d) out[d] = 0;
-        if (p.fill & 2) p.lse[row * p.heads + head] = -INFINITY;
-      }
+      if (mine < t.left && half == 0) put_nothing<T>(p, (int64_t)t.row + mine, head);
       continue;
     }
     const Range keys = p.kv_offsets ? rows_of(p.kv_offsets, p.batch, p.kv_tokens, t.sequence)
                                     : Range{t.first, t.row - t.first + t.left};
-    const SeenKeys seen(p.causal != 0, keys.count, t.left, BM, wave, lane);
+    const SeenKeys seen(p.causal, keys.count, t.left, BM, wave, 32);
+    const int seen_keys = seen.by(mine);
     const int count = seen.tile_any / BN + (seen.tile_any % BN != 0);
     const int kv_head = head / p.group;
     const S *vbase = (const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head;
@@ -136,7 +85,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
           [&](int i) { return by_row.read(k, i % KT * 32, i / KT); },
           [&](int i, const Operand<T> &a) { s[i % KT] = multiply(a, q[i / KT], s[i % KT]); });
       if (masked) {
-        const int left = seen.mine - base;
+        const int left = seen_keys - base;
 #pragma unroll
         for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -212,45 +161,10 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
       landed();  // nobody reads the tiles any more
     }
 
-    if (loose >= 0) {   // (weights are above zero, so the values add as they are)
-      for (int j = loose * BN; j < seen.wave_any; ++j) {
-        if (j >= seen.mine) continue;
-        const S *at = vbase + (int64_t)j * p.v.token;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = d * 32 + row_of(i, half);
-            const float x = e < p.dim ? load1<T>(at + e) : 0.0f;
-            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[d][i] += x;
-          }
-      }
-    }
-
+    if (loose >= 0)
+      add_others<T, DT>(o, vbase, p.v.token, p.dim, loose * BN, seen.wave_any, seen_keys, half);
     l += __uint_as_float(lane_xor<32>(__float_as_uint(l)));
-    if (mine < t.left) {
-      const int64_t row = (int64_t)t.row + mine;
-      S *out = (S *)p.out.data + row * p.out.token + head * p.out.head;
-      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int at = d * 32 + row_of(i, half);
-          if (at < p.dim) {
-            const f32x4_t w = {o[d][i] * inv, o[d][i + 1] * inv, o[d][i + 2] * inv,
-                               o[d][i + 3] * inv};
-            if constexpr (sizeof(S) == 4)
-              *reinterpret_cast<f32x4_t *>(out + at) = w;
-            else
-              *reinterpret_cast<u32x2_u *>(out + at) =
-                  u32x2_u{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
-          }
-        }
-      if (p.lse && half == 0)
-        p.lse[row * p.heads + head] =
-            l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
-    }
+    if (mine < t.left) put_row<T, DT>(p, o, m, l, (int64_t)t.row + mine, head, half);
   }
 }
 

@@ -143,8 +143,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 // Fills tiles one after another with the rows of a tensor: a wave's loads keep
-// their lanes' offsets, and only the buffer moves on (10 scalar instructions a tile;
-// with a buffer for each load there were 80, a sixth of the kernel's time).
+// their lanes' offsets, and only the buffer moves on.
 template <typename T, int ROWS, int DP, int WAVES>
 struct TileLoad {
   using S = typename T::S;
@@ -155,31 +154,28 @@ struct TileLoad {
   uint32_t from[LOADS];
   const S *next;        // the first row of the next tile
   int left;             // rows from there on (what lies behind becomes zeros)
-  int64_t step;         // elements of a tile's rows
-  uint32_t row_bytes, last_bytes;
+  int64_t stride;       // elements of a row
 
-  __device__ __forceinline__ TileLoad(int wave, int lane, int64_t row_stride, int dim) {
+  __device__ __forceinline__ TileLoad(int wave, int lane, int64_t row_stride, int dim)
+      : stride(row_stride) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int at = (i * WAVES + wave) * kWave + lane, r = at / L::C;
       const int c = ((at % L::C) ^ L::key(r & 15)) * L::E;
       from[i] = c < dim ? (uint32_t)((r * row_stride + c) * (int64_t)sizeof(S)) : kNowhere;
     }
-    step = row_stride * ROWS;
-    row_bytes = (uint32_t)row_stride * (uint32_t)sizeof(S);
-    last_bytes = (uint32_t)dim * (uint32_t)sizeof(S);
   }
   __device__ __forceinline__ void start(const S *base, int rows) {
     next = base;
     left = rows;
   }
   // The loads are on their way when this returns.
-  __device__ __forceinline__ void fill(LdsChunks lds, int wave) {
+  __device__ __forceinline__ void fill(LdsChunks lds, int dim, int wave) {
     const uint32_t rows = left < ROWS ? left : ROWS;
-    const auto b = buffer_of(next, (rows - 1) * row_bytes + last_bytes);
+    const auto b = buffer_of(next, ((rows - 1) * (uint32_t)stride + dim) * (uint32_t)sizeof(S));
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load_to_lds(b, from[i], lds + (i * WAVES + wave) * kWave);
-    next += step;
+    next += ROWS * stride;
     left -= ROWS;
   }
 };

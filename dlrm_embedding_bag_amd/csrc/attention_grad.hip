@@ -133,8 +133,8 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
     vload.start((const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head, keys.count);
     auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
-      kload.fill(k, wave);
-      vload.fill(v, wave);
+      kload.fill(k, p.dim, wave);
+      vload.fill(v, p.dim, wave);
     };
     auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       const int base = n * BN;
@@ -204,9 +204,13 @@ __device__ __forceinline__ void fill_stats(LdsFloats lds, const Stats &stats, in
   if (wave == WAVES - 1) load_to_lds(buffer_of(stats.minus_delta + at, n * 4), lane * 4, lds + kWave);
 }
 
-// Keys: dk and dv.  A lane holds one key of its wave's 32.
-template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys_kernel(AttentionGradParams p,
+// Keys: dk and dv.  A lane holds one key of its wave's 32.  GROUPS groups of WAVES
+// waves hold the same keys and take every GROUPS-th tile of rows, each from buffers
+// of its own; their sums meet in LDS at the end.  A key that many rows see makes a
+// long workgroup, and there are few of them (one for 128 keys of a key head): half
+// as long, they spread evenly over the CUs.
+template <typename T, int DP, int WAVES, int BN, int GROUPS>
+__global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void grad_keys_kernel(AttentionGradParams p,
                                                                  float *ws, int kv_heads,
                                                                  int64_t items) {
   using S = typename T::S;
@@ -214,10 +218,15 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys
   constexpr int BM = WAVES * 32, QT = BN / 32, STEPS = DP / 16, DT = DP / 32;
   constexpr int AHEAD = 1;
   constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
-  __shared__ u32x4_t q0[L::SIZE], g0[L::SIZE], q1[SECOND], g1[SECOND];
-  __shared__ float s0[2 * kWave], s1[2 * kWave];
+  __shared__ u32x4_t q0s[GROUPS * L::SIZE], g0s[GROUPS * L::SIZE];
+  __shared__ u32x4_t q1s[GROUPS * SECOND], g1s[GROUPS * SECOND];
+  __shared__ float s0s[GROUPS * 2 * kWave], s1s[GROUPS * 2 * kWave];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave = wave_of_all % WAVES, part = wave_of_all / WAVES;
+  const LdsChunks q0 = (LdsChunks)q0s, g0 = (LdsChunks)g0s, q1 = (LdsChunks)q1s,
+                  g1 = (LdsChunks)g1s;
+  const LdsFloats s0 = (LdsFloats)s0s, s1 = (LdsFloats)s1s;
   TileLoad<T, BN, DP, WAVES> qload(wave, lane, p.q.token, p.dim);
   TileLoad<T, BN, DP, WAVES> gload(wave, lane, p.grad.token, p.dim);
   ReadRows<T, BN, DP> by_row(lane);
@@ -225,7 +234,11 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys
   const float c = p.scale * kLog2e;
   const int32_t *key_offsets = p.kv_offsets ? p.kv_offsets : p.offsets;
   const Stats stats(ws, p.tokens, p.heads);
-  const uint32_t by_stat = half * 16;   // of the lane's first four rows; the others 8 apart
+  // (the group's buffers: their size is a power of two beyond what keys reach)
+  by_row.place += part * L::SIZE * 16;
+  by_column.place += part * L::SIZE * 16;
+  // of the lane's first four rows; the others are 8 apart
+  const uint32_t by_stat = half * 16 + part * 2 * kWave * 4;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     // (the first keys, which most rows see, come first)
@@ -236,7 +249,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // key of the tile
     if (t.sequence < 0) {
-      if (mine < t.left && half == 0) {
+      if (mine < t.left && half == 0 && part == 0) {
         const int64_t key = (int64_t)t.row + mine;
         S *dk = (S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head;
         S *dv = (S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head;
@@ -276,27 +289,43 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys
         v[s] = load_operand<T>(vat, s * 16 + half * 8, p.dim, there);
       }
     }
-    int64_t stat = 0;   // of the next tile's first row
     f32x16_t ok[DT], ov[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) ok[d] = ov[d] = f32x16_t{};
 
-    // tiles of rows, head by head of the group
-    auto start = [&](int h) __attribute__((always_inline)) {
-      const int64_t head = (int64_t)kv_head * p.group + h, row = rows.first + (int64_t)n0 * BN;
-      qload.start((const S *)p.q.data + row * p.q.token + head * p.q.head, rows.count - n0 * BN);
-      gload.start((const S *)p.grad.data + row * p.grad.token + head * p.grad.head,
-                  rows.count - n0 * BN);
-      stat = head * p.tokens + row;
+    // tiles of rows, head by head of the group: the next to be asked for
+    const int total = per_head > 0 ? per_head * p.group : 0;
+    const int rounds = total / GROUPS + (total % GROUPS != 0);
+    struct Place {
+      int head, tile;
     };
+    auto move = [&](Place &at, int n) __attribute__((always_inline)) {
+      at.tile += n;
+      while (at.tile >= per_head) {
+        at.tile -= per_head;
+        ++at.head;
+      }
+    };
+    Place asked{0, 0}, at_work{0, 0};
+    if (total) {
+      move(asked, part);
+      at_work = asked;
+    }
     auto fill = [&](LdsChunks q, LdsChunks g, LdsFloats st) __attribute__((always_inline)) {
-      fill_stats<BN, WAVES>(st, stats, stat, qload.left, wave, lane);
-      qload.fill(q, wave);
-      gload.fill(g, wave);
-      stat += BN;
+      if (asked.head >= p.group) return;
+      const int skip = (n0 + asked.tile) * BN, left = rows.count - skip;
+      const int64_t head = (int64_t)kv_head * p.group + asked.head, row = (int64_t)rows.first + skip;
+      qload.start((const S *)p.q.data + row * p.q.token + head * p.q.head, left);
+      gload.start((const S *)p.grad.data + row * p.grad.token + head * p.grad.head, left);
+      qload.fill(q + part * L::SIZE, p.dim, wave);
+      gload.fill(g + part * L::SIZE, p.dim, wave);
+      fill_stats<BN, WAVES>(st + part * 2 * kWave, stats, head * p.tokens + row, left, wave, lane);
+      move(asked, GROUPS);
     };
-    auto work = [&](LdsChunks q, LdsChunks g, LdsFloats st, int n) __attribute__((always_inline)) {
-      const int base = n * BN;
+    auto work = [&](LdsChunks q, LdsChunks g, LdsFloats st) __attribute__((always_inline)) {
+      if (at_work.head >= p.group) return;
+      const int base = (n0 + at_work.tile) * BN;
+      move(at_work, GROUPS);
       if (wave_from - base >= BN) return;
       const bool masked = base < wave_full;
 #pragma unroll
@@ -340,32 +369,60 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys
             });
       }
     };
-    for (int h = 0; h < p.group; ++h) {
-      if (per_head <= 0) break;
-      start(h);
-      if constexpr (WAVES == 1) {
-        for (int n = 0; n < per_head; ++n) {
-          fill((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0);
-          landed();
-          work((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0, n0 + n);
-          landed();
-        }
-      } else {
-        fill((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0);
-        for (int n = 0; n < per_head; n += 2) {
-          landed();
-          if (n + 1 < per_head) fill((LdsChunks)q1, (LdsChunks)g1, (LdsFloats)s1);
-          work((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0, n0 + n);
-          if (n + 1 < per_head) {
-            landed();
-            if (n + 2 < per_head) fill((LdsChunks)q0, (LdsChunks)g0, (LdsFloats)s0);
-            work((LdsChunks)q1, (LdsChunks)g1, (LdsFloats)s1, n0 + n + 1);
-          }
-        }
+    if constexpr (WAVES == 1) {
+      for (int n = 0; n < rounds; ++n) {
+        fill(q0, g0, s0);
+        landed();
+        work(q0, g0, s0);
         landed();
       }
+    } else {
+      if (rounds > 0) fill(q0, g0, s0);
+      for (int n = 0; n < rounds; n += 2) {
+        landed();
+        if (n + 1 < rounds) fill(q1, g1, s1);
+        work(q0, g0, s0);
+        if (n + 1 < rounds) {
+          landed();
+          if (n + 2 < rounds) fill(q0, g0, s0);
+          work(q1, g1, s1);
+        }
+      }
+      landed();
     }
-    if (mine < t.left) {
+    if constexpr (GROUPS == 2) {
+      // the second group's sums, 16 of a lane at a time, wherever a tile was
+      constexpr int EACH = GROUPS * L::SIZE * 16 / (WAVES * kWave * 64);   // of a buffer
+      static_assert(EACH >= 1 && EACH * 4 >= 2 * DT);
+      const LdsChunks buffers[4] = {(LdsChunks)q0s, (LdsChunks)g0s, (LdsChunks)q1s, (LdsChunks)g1s};
+      auto place = [&](int i, int e) {
+        return buffers[i / EACH] + (i % EACH * 4 + e) * WAVES * kWave + wave * kWave + lane;
+      };
+      if (part == 1) {
+#pragma unroll
+        for (int i = 0; i < 2 * DT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f32x16_t &a = i < DT ? ok[i] : ov[i - DT];
+            *place(i, e) = u32x4_t{__float_as_uint(a[4 * e]), __float_as_uint(a[4 * e + 1]),
+                                   __float_as_uint(a[4 * e + 2]), __float_as_uint(a[4 * e + 3])};
+          }
+      }
+      landed();
+      if (part == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * DT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const u32x4_t w = *place(i, e);
+            f32x16_t &a = i < DT ? ok[i] : ov[i - DT];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[4 * e + j] += __uint_as_float(w[j]);
+          }
+      }
+      landed();   // the buffers are free for the next item
+    }
+    if (mine < t.left && part == 0) {
       const int64_t key = (int64_t)t.row + mine;
       store_rows<T, DT>((S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head, ok, p.scale, half,
                         p.dim);
@@ -376,29 +433,51 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_keys
 }
 
 template <typename T, int DP, int WAVES, int BN>
-hipError_t run(const AttentionGradParams &p, float *ws, hipStream_t stream) {
-  const dim3 block(WAVES * kWave);
-  if (p.tokens) {
-    const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
-    launch_kernel(grad_rows_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), block, 0, stream, p,
-                  ws, items);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (!p.kv_tokens) return hipSuccess;
-  const int kv_heads = p.heads / p.group;
-  const int64_t items = tile_count(p.kv_tokens, p.batch, WAVES * 32) * kv_heads;
-  launch_kernel(grad_keys_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), block, 0, stream, p,
-                ws, kv_heads, items);
+hipError_t run_rows(const AttentionGradParams &p, float *ws, hipStream_t stream) {
+  const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
+  launch_kernel(grad_rows_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), dim3(WAVES * kWave), 0,
+                stream, p, ws, items);
   return hipGetLastError();
 }
 
-template <typename T, int WAVES, int BN>
+template <typename T, int DP, int WAVES, int BN, int GROUPS>
+hipError_t run_keys(const AttentionGradParams &p, float *ws, hipStream_t stream) {
+  const int kv_heads = p.heads / p.group;
+  const int64_t items = tile_count(p.kv_tokens, p.batch, WAVES * 32) * kv_heads;
+  launch_kernel(grad_keys_kernel<T, DP, WAVES, BN, GROUPS>, dim3(grid_of(items)),
+                dim3(WAVES * GROUPS * kWave), 0, stream, p, ws, kv_heads, items);
+  return hipGetLastError();
+}
+
+// Sequences of few rows take a wave each, and none waits for another (64 of 100
+// rows, 8 heads of 64: 35 us for 40).  Else a workgroup takes 128 rows or keys, but
+// 64 keys where that would leave CUs without one (2000 keys of two key heads: XX).
+template <typename T, int DP>
+hipError_t run(const AttentionGradParams &p, float *ws, hipStream_t stream) {
+  constexpr int BN = sizeof(typename T::S) == 4 ? 32 : 64;
+  const bool few = (p.tokens > p.kv_tokens ? p.tokens : p.kv_tokens) / p.batch <= 128;
+  if (p.tokens) {
+    const hipError_t e =
+        few ? run_rows<T, DP, 1, 32>(p, ws, stream) : run_rows<T, DP, 4, BN>(p, ws, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (!p.kv_tokens) return hipSuccess;
+  if (few) return run_keys<T, DP, 1, 32, 1>(p, ws, stream);
+  const int64_t wide = p.kv_tokens / 128 * (p.heads / p.group);
+  if constexpr (DP == 32) {
+    return run_keys<T, DP, 4, BN, 1>(p, ws, stream);
+  } else {
+    if (sizeof(typename T::S) == 2 && wide >= 256) return run_keys<T, DP, 4, BN, 2>(p, ws, stream);
+    return run_keys<T, DP, 2, BN, 2>(p, ws, stream);
+  }
+}
+
+template <typename T>
 hipError_t by_dim(const AttentionGradParams &p, float *ws, hipStream_t stream) {
-  if (p.dim <= 32) return run<T, 32, WAVES, BN>(p, ws, stream);
-  if (p.dim <= 64) return run<T, 64, WAVES, BN>(p, ws, stream);
-  if (p.dim <= 96) return run<T, 96, WAVES, BN>(p, ws, stream);
-  return run<T, 128, WAVES, BN>(p, ws, stream);
+  if (p.dim <= 32) return run<T, 32>(p, ws, stream);
+  if (p.dim <= 64) return run<T, 64>(p, ws, stream);
+  if (p.dim <= 96) return run<T, 96>(p, ws, stream);
+  return run<T, 128>(p, ws, stream);
 }
 
 }  // namespace
@@ -410,10 +489,7 @@ size_t attention_grad_workspace(int64_t tokens, int heads) {
 hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *workspace,
                                  hipStream_t stream) {
   float *ws = (float *)workspace;
-  const bool few = (p.tokens > p.kv_tokens ? p.tokens : p.kv_tokens) / p.batch <= 48;
-  if (dtype == kF32)
-    return few ? by_dim<F32, 1, 32>(p, ws, stream) : by_dim<F32, 4, 32>(p, ws, stream);
-  return few ? by_dim<BF16, 1, 32>(p, ws, stream) : by_dim<BF16, 4, 64>(p, ws, stream);
+  return dtype == kF32 ? by_dim<F32>(p, ws, stream) : by_dim<BF16>(p, ws, stream);
 }
 
 }  // namespace dlrm

@@ -71,8 +71,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
     vload.start(vbase, keys.count);
     auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
-      kload.fill(k, wave);
-      vload.fill(v, wave);
+      kload.fill(k, p.dim, wave);
+      vload.fill(v, p.dim, wave);
     };
     auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       const int base = n * BN;
@@ -188,7 +188,8 @@ hipError_t by_dim(const AttentionParams &p, hipStream_t stream) {
 
 hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream) {
   // sequences of few rows take a wave each, and none waits for another
-  const bool few = p.tokens / p.batch <= 48;
+  // (64 of 100 rows, 8 heads of 64: 12 us for 17 in bfloat16, 23 for 38 in float32)
+  const bool few = p.tokens / p.batch <= 128;
   if (dtype == kF32) return few ? by_dim<F32, 1, 32>(p, stream) : by_dim<F32, 4, 32>(p, stream);
   return few ? by_dim<BF16, 1, 32>(p, stream) : by_dim<BF16, 4, 64>(p, stream);
 }

@@ -143,7 +143,8 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 // Fills tiles one after another with the rows of a tensor: a wave's loads keep
-// their lanes' offsets, and only the buffer moves on.
+// their lanes' offsets, and only the buffer moves on.  Behind the last row a tile
+// holds zeros, or where rows repeat (a stride below their length) one of them.
 template <typename T, int ROWS, int DP, int WAVES>
 struct TileLoad {
   using S = typename T::S;
@@ -153,7 +154,7 @@ struct TileLoad {
   static constexpr uint32_t kNowhere = 0x80000000u;   // beyond any tile: reads as zeros
   uint32_t from[LOADS];
   const S *next;        // the first row of the next tile
-  int left;             // rows from there on (what lies behind becomes zeros)
+  int left;             // rows from there on
   int64_t stride;       // elements of a row
 
   __device__ __forceinline__ TileLoad(int wave, int lane, int64_t row_stride, int dim)

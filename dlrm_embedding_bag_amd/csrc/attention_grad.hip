@@ -20,13 +20,18 @@
 namespace dlrm {
 namespace {
 
-// What the second kernel needs of a row, head by head in planes of `tokens`:
-// lse in units of log 2, +inf where the row sees nothing, and then -delta.
+// What the second kernel needs of a row, head by head in planes of `tokens`: lse in
+// units of log 2, +inf where the row sees nothing, with the bits of +inf turned so
+// that the zeros that are read behind the last row stand for it, too; and -delta.
+constexpr uint32_t kInfinity = 0x7f800000u;
 struct Stats {
-  float *lse2, *minus_delta;
+  float *turned_lse2, *minus_delta;
   __host__ __device__ Stats(float *at, int64_t tokens, int64_t heads)
-      : lse2(at), minus_delta(at + tokens * heads) {}
+      : turned_lse2(at), minus_delta(at + tokens * heads) {}
 };
+__device__ __forceinline__ float turned(float lse2) {
+  return __uint_as_float(__float_as_uint(lse2) ^ kInfinity);
+}
 
 template <typename T, int DT>
 __device__ __forceinline__ void store_rows(typename T::S *out, const f32x16_t (&o)[DT],
@@ -123,7 +128,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     if (lse2 == -INFINITY) lse2 = INFINITY;
     if (there && half == 0) {
       const Stats stats(ws, p.tokens, p.heads);
-      stats.lse2[head * p.tokens + row] = lse2;
+      stats.turned_lse2[head * p.tokens + row] = turned(lse2);
       stats.minus_delta[head * p.tokens + row] = -delta;
     }
 
@@ -193,14 +198,13 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
   }
 }
 
-// The statistics of a tile's rows, 64 a load; behind the last row zeros (whose
-// gradient is zero, too, so they add nothing).
+// The statistics of a tile's rows, 64 a load; zeros behind the last row.
 template <int BN, int WAVES>
 __device__ __forceinline__ void fill_stats(LdsFloats lds, const Stats &stats, int64_t at, int rows,
                                            int wave, int lane) {
   static_assert(BN <= kWave);
   const int n = rows < BN ? rows : BN;
-  if (wave == 0) load_to_lds(buffer_of(stats.lse2 + at, n * 4), lane * 4, lds);
+  if (wave == 0) load_to_lds(buffer_of(stats.turned_lse2 + at, n * 4), lane * 4, lds);
   if (wave == WAVES - 1) load_to_lds(buffer_of(stats.minus_delta + at, n * 4), lane * 4, lds + kWave);
 }
 
@@ -341,7 +345,7 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
           const f32x4_t from = lds_at<f32x4_t>((LdsBytes)st, by_stat + (kWave + j * 32 + i * 2) * 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -lse2[e]));
+            s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -turned(lse2[e])));
             dp[i + e] = from[e];
           }
         }

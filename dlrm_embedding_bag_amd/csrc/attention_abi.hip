@@ -4,6 +4,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <initializer_list>
+
 #include "../../include/dlrm_embedding_bag.h"
 #include "kernels.hpp"
 
@@ -44,8 +46,13 @@ bool aligned_rows(const void *p, int64_t n, int64_t token, int32_t heads, int64_
   const int64_t e = 16 / size_of(dtype);
   return aligned16(p) && (n <= 1 || token % e == 0) && (heads <= 1 || head % e == 0);
 }
-// Tiles of 64 rows are addressed within 32 bits.
-constexpr int64_t kMaxTokenStride = 1 << 22;
+// Tiles of up to 128 rows are addressed within 2 GiB.
+constexpr int64_t kMaxTokenStride = (1 << 22) - 1024;
+bool near_rows(int64_t n, std::initializer_list<int64_t> strides) {
+  for (const int64_t s : strides)
+    if (n > 1 && s > kMaxTokenStride) return false;
+  return true;
+}
 
 int attention_shape(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t heads,
                     int32_t kv_heads, int32_t dim, int32_t dtype, int32_t causal, float scale) {
@@ -165,7 +172,7 @@ int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t h
       !aligned_rows(v, kv_tokens, v_token, kv_heads, v_head, dtype) ||
       !aligned_rows(out, tokens, o_token, heads, o_head, dtype))
     return DLRM_ERR_UNSUPPORTED;
-  if (kv_tokens > 1 && (k_token > kMaxTokenStride || v_token > kMaxTokenStride))
+  if (!near_rows(tokens, {q_token, o_token}) || !near_rows(kv_tokens, {k_token, v_token}))
     return DLRM_ERR_UNSUPPORTED;
   AttentionParams p{};
   p.tokens = tokens;
@@ -174,7 +181,7 @@ int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t h
   p.heads = heads;
   p.group = heads / kv_heads;
   p.dim = dim;
-  p.q = {q, q_token, q_head};
+  p.q = {q, tokens > 1 ? q_token : dim, q_head};
   p.k = {k, kv_tokens > 1 ? k_token : dim, k_head};
   p.v = {v, kv_tokens > 1 ? v_token : dim, v_head};
   p.offsets = offsets;
@@ -182,7 +189,7 @@ int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t h
   p.causal = causal;
   p.scale = scale;
   p.fill = lse ? fill : fill & 1;
-  p.out = {out, o_token, o_head};
+  p.out = {out, tokens > 1 ? o_token : dim, o_head};
   p.lse = lse;
   return status_of(launch_attention(p, dtype, (hipStream_t)stream));
 }
@@ -227,8 +234,8 @@ int attention_packed_grad(int64_t tokens, int64_t kv_tokens, int64_t batch, int3
       !aligned_rows(dk, kv_tokens, dk_token, kv_heads, dk_head, dtype) ||
       !aligned_rows(dv, kv_tokens, dv_token, kv_heads, dv_head, dtype))
     return DLRM_ERR_UNSUPPORTED;
-  if ((kv_tokens > 1 && (k_token > kMaxTokenStride || v_token > kMaxTokenStride)) ||
-      (tokens > 1 && (q_token > kMaxTokenStride || g_token > kMaxTokenStride)))
+  if (!near_rows(tokens, {q_token, g_token, o_token, dq_token}) ||
+      !near_rows(kv_tokens, {k_token, v_token, dk_token, dv_token}))
     return DLRM_ERR_UNSUPPORTED;
   const size_t need = attention_grad_workspace(tokens, heads);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
@@ -244,16 +251,16 @@ int attention_packed_grad(int64_t tokens, int64_t kv_tokens, int64_t batch, int3
   p.q = {q, tokens > 1 ? q_token : dim, q_head};
   p.k = {k, kv_tokens > 1 ? k_token : dim, k_head};
   p.v = {v, kv_tokens > 1 ? v_token : dim, v_head};
-  p.out = {out, o_token, o_head};
+  p.out = {out, tokens > 1 ? o_token : dim, o_head};
   p.lse = lse;
   p.offsets = offsets;
   p.kv_offsets = kv_offsets;
   p.causal = causal;
   p.scale = scale;
   p.fill = fill;
-  p.dq = {dq, dq_token, dq_head};
-  p.dk = {dk, dk_token, dk_head};
-  p.dv = {dv, dv_token, dv_head};
+  p.dq = {dq, tokens > 1 ? dq_token : dim, dq_head};
+  p.dk = {dk, kv_tokens > 1 ? dk_token : dim, dk_head};
+  p.dv = {dv, kv_tokens > 1 ? dv_token : dim, dv_head};
   return status_of(launch_attention_grad(p, dtype, workspace, (hipStream_t)stream));
 }
 

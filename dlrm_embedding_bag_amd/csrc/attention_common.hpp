@@ -11,6 +11,7 @@ namespace dlrm {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -70,23 +71,6 @@ __device__ __forceinline__ Operand<T> zero_operand() {
   return o;
 }
 
-// Eight elements from c on of a row of memory, zeros where there is no row or
-// c lies beyond its end (rows hold a multiple of eight).
-template <typename T>
-__device__ __forceinline__ Operand<T> load_operand(const typename T::S *row, int c, int dim,
-                                                   bool there) {
-  Operand<T> o = zero_operand<T>();
-  if (there && c < dim) {
-    if constexpr (sizeof(typename T::S) == 4) {
-      o.v[0] = *reinterpret_cast<const f32x4_t *>(row + c);
-      o.v[1] = *reinterpret_cast<const f32x4_t *>(row + c + 4);
-    } else {
-      o.v = *reinterpret_cast<const u32x4_t *>(row + c);
-    }
-  }
-  return o;
-}
-
 // ------------------------------------------------------------ tiles in LDS --
 // ROWS rows of DP elements as chunks of 16 bytes, C places a row.  LDS serves 256
 // bytes at once: 16 lanes of a row's read (16 rows, one chunk), 32 of a transposed
@@ -121,11 +105,22 @@ typedef __attribute__((address_space(3))) u32x4_t *LdsChunks;
 typedef __attribute__((address_space(3))) float *LdsFloats;
 typedef const __attribute__((address_space(3))) char *LdsBytes;
 
-// `bytes` of memory from `base` on, behind which loads read zeros.  (These two
-// are no templates: the host's pass drops kernels whose templates call such
-// builtins twice.)
+// `bytes` of memory from `base` on, behind which loads read zeros.  (These are no
+// templates: the host's pass drops kernels whose templates call such builtins
+// twice.)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 4 << 15);
+}
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset beyond any such buffer
+// 16 bytes from there to registers, and 16 or 8 back; stores beyond it do nothing.
+__device__ __forceinline__ u32x4_t load_from(__amdgpu_buffer_rsrc_t b, uint32_t from) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(b, from, 0, 0));
+}
+__device__ __forceinline__ void store_to(__amdgpu_buffer_rsrc_t b, uint32_t to, u32x4_t v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, b, to, 0, 0);
+}
+__device__ __forceinline__ void store_to(__amdgpu_buffer_rsrc_t b, uint32_t to, u32x2_t v) {
+  __builtin_amdgcn_raw_buffer_store_b64(v, b, to, 0, 0);
 }
 // 16 or 4 bytes a lane, from memory to LDS: lane l's to lds[l].
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t from,
@@ -151,7 +146,6 @@ struct TileLoad {
   using L = LdsTile<T, ROWS, DP>;
   static constexpr int LOADS = L::SIZE / (WAVES * kWave);
   static_assert(L::SIZE % (WAVES * kWave) == 0 && WAVES * kWave % L::C == 0);
-  static constexpr uint32_t kNowhere = 0x80000000u;   // beyond any tile: reads as zeros
   uint32_t from[LOADS];
   const S *next;        // the first row of the next tile
   int left;             // rows from there on
@@ -163,7 +157,7 @@ struct TileLoad {
     for (int i = 0; i < LOADS; ++i) {
       const int at = (i * WAVES + wave) * kWave + lane, r = at / L::C;
       const int c = ((at % L::C) ^ L::key(r & 15)) * L::E;
-      from[i] = c < dim ? (uint32_t)((r * row_stride + c) * (int64_t)sizeof(S)) : kNowhere;
+      from[i] = c < dim ? ((uint32_t)r * (uint32_t)row_stride + c) * (uint32_t)sizeof(S) : kNowhere;
     }
   }
   __device__ __forceinline__ void start(const S *base, int rows) {
@@ -178,6 +172,51 @@ struct TileLoad {
     for (int i = 0; i < LOADS; ++i) load_to_lds(b, from[i], lds + (i * WAVES + wave) * kWave);
     next += ROWS * stride;
     left -= ROWS;
+  }
+};
+
+// A lane's row of a tile of rows in memory: rows from `base` on, of which `left`
+// are there.  What lies behind them or behind a row's end reads as zeros and is not
+// stored.
+template <typename T>
+struct MemoryRow {
+  using S = typename T::S;
+  __amdgpu_buffer_rsrc_t buffer;
+  uint32_t row;   // offset of the lane's
+  int dim;
+  __device__ __forceinline__ MemoryRow(const void *base, int64_t stride, int left, int dim_, int r)
+      : buffer(buffer_of(base, ((uint32_t)(left < 128 ? left - 1 : 127) * (uint32_t)stride + dim_) *
+                                   (uint32_t)sizeof(S))),
+        row(r < left ? (uint32_t)r * (uint32_t)stride * (uint32_t)sizeof(S) : kNowhere), dim(dim_) {}
+  // Elements 8 c on.
+  __device__ __forceinline__ Operand<T> load(int c) const {
+    const uint32_t from = c < dim ? row + c * (uint32_t)sizeof(S) : kNowhere;
+    Operand<T> o;
+    if constexpr (sizeof(S) == 4) {
+      o.v[0] = __builtin_bit_cast(f32x4_t, load_from(buffer, from));
+      o.v[1] = __builtin_bit_cast(f32x4_t, load_from(buffer, from + 16));
+    } else {
+      o.v = load_from(buffer, from);
+    }
+    return o;
+  }
+  // A lane's half of a row: what its columns of products hold, times `scale`.
+  template <int DT>
+  __device__ __forceinline__ void store(const f32x16_t (&o)[DT], float scale, int half) const {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int c = d * 32 + row_of(i, half);
+        const uint32_t to = c < dim ? row + c * (uint32_t)sizeof(S) : kNowhere;
+        const float w[4] = {o[d][i] * scale, o[d][i + 1] * scale, o[d][i + 2] * scale,
+                            o[d][i + 3] * scale};
+        if constexpr (sizeof(S) == 4)
+          store_to(buffer, to, u32x4_t{__float_as_uint(w[0]), __float_as_uint(w[1]),
+                                       __float_as_uint(w[2]), __float_as_uint(w[3])});
+        else
+          store_to(buffer, to, u32x2_t{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])});
+      }
   }
 };
 
@@ -306,44 +345,45 @@ struct Tile {
 
 // Where segment s begins, and the last one ends; offsets that a bad array holds
 // are moved into the tensor.
-__device__ __forceinline__ int64_t segment_start(const int32_t *offsets, int64_t batch,
-                                                 int64_t total, int64_t s) {
-  if (s <= 0) return 0;
+__device__ __forceinline__ int segment_start(const int32_t *offsets, uint32_t batch, int total,
+                                             uint32_t s) {
+  if (s == 0) return 0;
   if (s > batch + 1) return total;
-  const int64_t o = offsets[s - 1];
+  const int o = offsets[s - 1];
   return o < 0 ? 0 : o > total ? total : o;
 }
 
 __host__ __device__ inline int64_t tile_count(int64_t total, int64_t batch, int rows) {
-  return total / rows + batch + 2;
+  return total / rows + batch + 2;   // (below 2^32)
 }
 
 // Every lane of the wave takes part; the result is the same in all.
-__device__ __forceinline__ Tile find_tile(const int32_t *offsets, int64_t batch, int64_t total,
-                                          int64_t tile, int rows) {
-  const int lane = threadIdx.x % kWave;
-  int64_t lo = 0, n = batch + 2;  // the segment is one of [lo, lo + n)
+__device__ __forceinline__ Tile find_tile(const int32_t *offsets, uint32_t batch, int total,
+                                          uint32_t tile, uint32_t rows) {
+  const uint32_t lane = threadIdx.x % kWave;
+  uint32_t lo = 0, n = batch + 2;  // the segment is one of [lo, lo + n)
   while (n > 1) {
-    const int64_t step = (n + kWave - 1) / kWave;
-    const int64_t s = lo + lane * step;
+    const uint32_t step = (n - 1) / kWave + 1;
+    const uint32_t s = lo + lane * step;   // (below 2^32: n is below 2^31 + 2)
     bool before = false;
-    if (s < lo + n) before = segment_start(offsets, batch, total, s) / rows + s <= tile;
+    if (lane * step < n)
+      before = (uint32_t)segment_start(offsets, batch, total, s) / rows + s <= tile;
     const uint64_t mask = __ballot(before);
-    const int64_t last = mask ? 63 - __clzll(mask) : 0;
-    const int64_t end = lo + n;
-    lo += last * step;
-    n = end - lo < step ? end - lo : step;
+    const uint32_t last = mask ? 63 - __clzll(mask) : 0;
+    lo = (uint32_t)uniform((int)(lo + last * step));
+    n = n - last * step < step ? n - last * step : step;
+    n = (uint32_t)uniform((int)n);
   }
-  lo = uniform(lo);
-  const int64_t first = uniform(segment_start(offsets, batch, total, lo));
-  const int64_t last = uniform(segment_start(offsets, batch, total, lo + 1));
-  const int64_t k = tile - (first / rows + lo);
-  const int64_t row = k < 0 ? last : first + k * rows;
+  const int first = uniform(segment_start(offsets, batch, total, lo));
+  const int last = uniform(segment_start(offsets, batch, total, lo + 1));
+  const uint32_t start = (uint32_t)first / rows + lo;
+  const uint64_t row = (uint64_t)first + (uint64_t)(tile - start) * rows;
   Tile t;
   t.sequence = lo >= 1 && lo <= batch ? (int)lo - 1 : -1;
-  t.first = (int)first;
-  t.left = row < last ? (int)(last - row) : 0;
-  t.row = (int)(row < last ? row : last);
+  t.first = first;
+  const bool there = tile >= start && row < (uint64_t)(last > 0 ? last : 0);
+  t.left = there ? (int)(last - (int64_t)row) : 0;
+  t.row = there ? (int)row : last;
   return t;
 }
 
@@ -351,10 +391,9 @@ __device__ __forceinline__ Tile find_tile(const int32_t *offsets, int64_t batch,
 struct Range {
   int first, count;
 };
-__device__ __forceinline__ Range rows_of(const int32_t *offsets, int64_t batch, int64_t total,
-                                         int b) {
-  const int first = uniform((int)segment_start(offsets, batch, total, (int64_t)b + 1));
-  const int last = uniform((int)segment_start(offsets, batch, total, (int64_t)b + 2));
+__device__ __forceinline__ Range rows_of(const int32_t *offsets, uint32_t batch, int total, int b) {
+  const int first = uniform(segment_start(offsets, batch, total, (uint32_t)b + 1));
+  const int last = uniform(segment_start(offsets, batch, total, (uint32_t)b + 2));
   return {first, last > first ? last - first : 0};
 }
 
@@ -384,11 +423,11 @@ struct SeenKeys {
 };
 
 // Item `i` of tiles * heads.  The last tiles come first: with `causal` they see
-// the most keys, and work that ends early should be short (four prompts of up to
-// 6500: X us for Y).  Workgroups go to the eight dies in turn, so a die gets heads
-// that lie together, whose key heads then share its cache.
+// the most keys, and work that ends early should be short.  Workgroups go to the
+// eight dies in turn, so a die gets heads that lie together, whose key heads then
+// share its cache (both together: four prompts of up to 6500 rows 955 us for 1019).
 struct Item {
-  int64_t tile;
+  uint32_t tile;
   int head;
 };
 __device__ __forceinline__ Item item_of(int64_t i, int64_t tiles, int heads) {
@@ -403,7 +442,7 @@ __device__ __forceinline__ Item item_of(int64_t i, int64_t tiles, int heads) {
     r = (uint32_t)n - (uint32_t)t * (uint32_t)heads;
   }
   if (heads % 8 == 0) r = r % 8 * (heads / 8) + r / 8;
-  return {tiles - 1 - t, (int)r};
+  return {(uint32_t)(tiles - 1 - t), (int)r};
 }
 
 // Workgroups for that many items; each takes those a grid apart.

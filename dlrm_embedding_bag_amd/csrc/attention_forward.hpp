@@ -75,27 +75,13 @@ __device__ __forceinline__ void add_others(f32x16_t (&o)[DT], const typename T::
 // A lane's half of a row: its sums relative to m, l the row's whole.
 template <typename T, int DT>
 __device__ __forceinline__ void put_row(const AttentionParams &p, const f32x16_t (&o)[DT], float m,
-                                        float l, int64_t row, int head, int half) {
+                                        float l, const Tile &t, int mine, int head, int half) {
   using S = typename T::S;
-  S *out = (S *)p.out.data + row * p.out.token + head * p.out.head;
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int at = d * 32 + row_of(i, half);
-      if (at < p.dim) {
-        const f32x4_t w = {o[d][i] * inv, o[d][i + 1] * inv, o[d][i + 2] * inv,
-                           o[d][i + 3] * inv};
-        if constexpr (sizeof(S) == 4)
-          *reinterpret_cast<f32x4_t *>(out + at) = w;
-        else
-          *reinterpret_cast<u32x2_u *>(out + at) =
-              u32x2_u{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
-      }
-    }
-  if (p.lse && half == 0)
-    p.lse[row * p.heads + head] =
+  const MemoryRow<T> out((S *)p.out.data + t.row * p.out.token + head * p.out.head, p.out.token,
+                         t.left, p.dim, mine);
+  out.store(o, l > 0.0f || l != l ? 1.0f / l : 0.0f, half);
+  if (p.lse && half == 0 && mine < t.left)
+    p.lse[((int64_t)t.row + mine) * p.heads + head] =
         l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
 }
 

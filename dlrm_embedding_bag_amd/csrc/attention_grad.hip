@@ -33,26 +33,6 @@ __device__ __forceinline__ float turned(float lse2) {
   return __uint_as_float(__float_as_uint(lse2) ^ kInfinity);
 }
 
-template <typename T, int DT>
-__device__ __forceinline__ void store_rows(typename T::S *out, const f32x16_t (&o)[DT],
-                                           float scale, int half, int dim) {
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int at = d * 32 + row_of(i, half);
-      if (at < dim) {
-        const f32x4_t w = {o[d][i] * scale, o[d][i + 1] * scale, o[d][i + 2] * scale,
-                           o[d][i + 3] * scale};
-        if constexpr (sizeof(typename T::S) == 4)
-          *reinterpret_cast<f32x4_t *>(out + at) = w;
-        else
-          *reinterpret_cast<u32x2_u *>(out + at) =
-              u32x2_u{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
-      }
-    }
-}
-
 template <typename T>
 __device__ __forceinline__ float dot(const Operand<T> &a, const Operand<T> &b, float sum) {
   if constexpr (sizeof(typename T::S) == 4) {
@@ -112,15 +92,18 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     Operand<T> q[STEPS], g[STEPS];
     float delta = 0.0f;
     {
-      const S *qat = (const S *)p.q.data + row * p.q.token + head * p.q.head;
-      const S *gat = (const S *)p.grad.data + row * p.grad.token + head * p.grad.head;
-      const S *oat = (const S *)p.out.data + row * p.out.token + head * p.out.head;
+      const MemoryRow<T> qs((const S *)p.q.data + t.row * p.q.token + head * p.q.head, p.q.token,
+                            t.left, p.dim, mine);
+      const MemoryRow<T> gs((const S *)p.grad.data + t.row * p.grad.token + head * p.grad.head,
+                            p.grad.token, t.left, p.dim, mine);
+      const MemoryRow<T> os((const S *)p.out.data + t.row * p.out.token + head * p.out.head,
+                            p.out.token, t.left, p.dim, mine);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const int at = s * 16 + half * 8;
-        q[s] = load_operand<T>(qat, at, p.dim, there);
-        g[s] = load_operand<T>(gat, at, p.dim, there);
-        delta = dot<T>(g[s], load_operand<T>(oat, at, p.dim, there), delta);
+        q[s] = qs.load(at);
+        g[s] = gs.load(at);
+        delta = dot<T>(g[s], os.load(at), delta);
       }
     }
     delta += __uint_as_float(lane_xor<32>(__float_as_uint(delta)));
@@ -145,7 +128,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
       const int base = n * BN;
       if (base >= seen.wave_any) return;
       const bool masked = seen.wave_all - base < BN;
-      const int left = seen_keys - base;
+      const int left = seen_keys - base - half * 4;
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
         f32x16_t s = f32x16_t{}, dp = f32x16_t{};
@@ -163,7 +146,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (j * 32 + row_of(i, half) >= left) s[i] = 0.0f;
+            if (j * 32 + row_of(i, 0) >= left) s[i] = 0.0f;
         }
         const Operand<T> w[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
         in_order<T, 2 * DT, AHEAD, true>(
@@ -192,9 +175,9 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
       }
       landed();
     }
-    if (mine < t.left)
-      store_rows<T, DT>((S *)p.dq.data + ((int64_t)t.row + mine) * p.dq.token + head * p.dq.head,
-                        o, p.scale, half, p.dim);
+    MemoryRow<T>((S *)p.dq.data + t.row * p.dq.token + head * p.dq.head, p.dq.token, t.left, p.dim,
+                 mine)
+        .store(o, p.scale, half);
   }
 }
 
@@ -283,14 +266,14 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
 
     Operand<T> k[STEPS], v[STEPS];
     {
-      const int64_t key = (int64_t)t.row + mine;
-      const bool there = mine < t.left;
-      const S *kat = (const S *)p.k.data + key * p.k.token + kv_head * p.k.head;
-      const S *vat = (const S *)p.v.data + key * p.v.token + kv_head * p.v.head;
+      const MemoryRow<T> ks((const S *)p.k.data + t.row * p.k.token + kv_head * p.k.head, p.k.token,
+                            t.left, p.dim, mine);
+      const MemoryRow<T> vs((const S *)p.v.data + t.row * p.v.token + kv_head * p.v.head, p.v.token,
+                            t.left, p.dim, mine);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
-        k[s] = load_operand<T>(kat, s * 16 + half * 8, p.dim, there);
-        v[s] = load_operand<T>(vat, s * 16 + half * 8, p.dim, there);
+        k[s] = ks.load(s * 16 + half * 8);
+        v[s] = vs.load(s * 16 + half * 8);
       }
     }
     f32x16_t ok[DT], ov[DT];
@@ -355,10 +338,10 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] *= s[i];
         if (masked) {
-          const int from = from_row - base;   // rows of the tile before it do not see the key
+          const int from = from_row - base - half * 4;   // rows of the tile before it do not see the key
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (j * 32 + row_of(i, half) < from) s[i] = dp[i] = 0.0f;
+            if (j * 32 + row_of(i, 0) < from) s[i] = dp[i] = 0.0f;
         }
         const Operand<T> wp[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
         const Operand<T> wd[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
@@ -426,12 +409,13 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
       }
       landed();   // the buffers are free for the next item
     }
-    if (mine < t.left && part == 0) {
-      const int64_t key = (int64_t)t.row + mine;
-      store_rows<T, DT>((S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head, ok, p.scale, half,
-                        p.dim);
-      store_rows<T, DT>((S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head, ov, 1.0f, half,
-                        p.dim);
+    if (part == 0) {
+      MemoryRow<T>((S *)p.dk.data + t.row * p.dk.token + kv_head * p.dk.head, p.dk.token, t.left,
+                   p.dim, mine)
+          .store(ok, p.scale, half);
+      MemoryRow<T>((S *)p.dv.data + t.row * p.dv.token + kv_head * p.dv.head, p.dv.token, t.left,
+                   p.dim, mine)
+          .store(ov, 1.0f, half);
     }
   }
 }

@@ -57,10 +57,10 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     const S *vbase = (const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head;
     Operand<T> q[STEPS];
     {
-      const S *at = (const S *)p.q.data + ((int64_t)t.row + mine) * p.q.token + head * p.q.head;
+      const MemoryRow<T> from((const S *)p.q.data + t.row * p.q.token + head * p.q.head, p.q.token,
+                              t.left, p.dim, mine);
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-        q[s] = load_operand<T>(at, s * 16 + half * 8, p.dim, mine < t.left);
+      for (int s = 0; s < STEPS; ++s) q[s] = from.load(s * 16 + half * 8);
     }
     f32x16_t o[DT];
 #pragma unroll
@@ -85,12 +85,12 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
           [&](int i) { return by_row.read(k, i % KT * 32, i / KT); },
           [&](int i, const Operand<T> &a) { s[i % KT] = multiply(a, q[i / KT], s[i % KT]); });
       if (masked) {
-        const int left = seen_keys - base;
+        const int left = seen_keys - base - half * 4;
 #pragma unroll
         for (int j = 0; j < KT; ++j)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (j * 32 + row_of(i, half) >= left) s[j][i] = -INFINITY;
+            if (j * 32 + row_of(i, 0) >= left) s[j][i] = -INFINITY;
       }
       float top = s[0][0];
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     if (loose >= 0)
       add_others<T, DT>(o, vbase, p.v.token, p.dim, loose * BN, seen.wave_any, seen_keys, half);
     l += __uint_as_float(lane_xor<32>(__float_as_uint(l)));
-    if (mine < t.left) put_row<T, DT>(p, o, m, l, (int64_t)t.row + mine, head, half);
+    put_row<T, DT>(p, o, m, l, t, mine, head, half);
   }
 }
 

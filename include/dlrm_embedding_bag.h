@@ -755,8 +755,8 @@ DLRM_API int qk_norm_rope_grad(
  *   heads       a multiple of kv_heads, which is >= 1
  *   dim         a multiple of 8 (DLRM_ERR_SHAPE); beyond DLRM_MAX_ATTENTION_DIM
  *               DLRM_ERR_UNSUPPORTED
- *   q, k, v, out  on 16 bytes, strides of multiples of 16 bytes; token strides
- *               of k and v up to 2^22 elements (else DLRM_ERR_UNSUPPORTED)
+ *   q, k, v, out  on 16 bytes, strides of multiples of 16 bytes, token strides
+ *               up to 2^22 - 1024 elements (else DLRM_ERR_UNSUPPORTED)
  *   offsets     (batch + 1,) int32, not decreasing, within [0, tokens]
  *   kv_offsets  the same for k and v, or NULL where they are offsets (then
  *               kv_tokens is tokens).  Offsets that are out of order give
@@ -788,7 +788,6 @@ DLRM_API int attention_packed(int64_t tokens, int64_t kv_tokens, int64_t batch, 
  * but none of another.
  *
  *   grad, out   as out in attention_packed; lse (tokens, heads) as it wrote it
- *   q, grad     token strides up to 2^22 elements, as those of k and v
  *   fill        rows outside all sequences: 0 they are left as they are; + 1
  *               they are zero in dq, + 2 in dk, + 4 in dv
  *   dq, dk, dv  as q, k, v; they must not overlap the inputs

@@ -117,7 +117,8 @@ def test_packed_refusals(lib):
         assert _status(lib, _packed(**bad)) == SHAPE, bad
     for bad in (dict(dim=136, qh=136, ot=544, oh=136), dict(q=FAKE + 4), dict(k=FAKE + 8),
                 dict(v=FAKE + 2), dict(out=FAKE + 4), dict(qt=258), dict(kt=130), dict(vh=66),
-                dict(ot=258), dict(dt=BF16, kt=132), dict(kt=(1 << 22) + 8), dict(vt=1 << 23)):
+                dict(ot=258), dict(dt=BF16, kt=132), dict(kt=(1 << 22) + 8), dict(vt=1 << 23),
+                dict(qt=1 << 22), dict(ot=1 << 22)):
         assert _status(lib, _packed(**bad)) == UNSUPPORTED, bad
     for name in ("q", "k", "v", "off", "out"):
         assert _status(lib, _packed(**{name: None})) == NULL, name
@@ -131,7 +132,8 @@ def test_packed_gradient_refusals(lib):
         assert _status(lib, _packed_grad(**bad)) == SHAPE, bad
     for bad in (dict(dim=136, dqt=544, dkt=272), dict(g=FAKE + 4), dict(q=FAKE + 8), dict(k=FAKE + 4),
                 dict(v=FAKE + 4), dict(o=FAKE + 4), dict(dq=FAKE + 4), dict(dk=FAKE + 8),
-                dict(dv=FAKE + 8), dict(gt=258), dict(gt=1 << 23), dict(kt=1 << 23)):
+                dict(dv=FAKE + 8), dict(gt=258), dict(gt=1 << 23), dict(kt=1 << 23),
+                dict(dqt=1 << 22), dict(dkt=1 << 22)):
         assert _status(lib, _packed_grad(**bad)) == UNSUPPORTED, bad
     for name in ("g", "q", "k", "v", "o", "lse", "off", "dq", "dk", "dv"):
         assert _status(lib, _packed_grad(**{name: None})) == NULL, name
@@ -205,11 +207,15 @@ def test_launches_hold_fewer_than_2_to_32_threads(launches):  # noqa: F811
                 for dim in (8, 40, 96, 128):
                     for dt in (F32, BF16):
                         t, kt = h * dim, kv * dim
-                        calls.append(_packed(n=n, m=n, b=b, h=h, kv=kv, dim=dim, dt=dt, qt=t, qh=dim,
-                                             kt=kt, kh=dim, vt=kt, vh=dim, ot=t, oh=dim))
-                        if t <= 1 << 22:
+                        if t <= 1 << 21:
+                            calls.append(_packed(n=n, m=n, b=b, h=h, kv=kv, dim=dim, dt=dt, qt=t,
+                                                 qh=dim, kt=kt, kh=dim, vt=kt, vh=dim, ot=t, oh=dim))
                             calls.append(_packed_grad(n=n, m=n, b=b, h=h, kv=kv, dim=dim, dt=dt, gt=t,
                                                       qt=t, kt=kt, vt=kt, dqt=t, dkt=kt))
+                        else:     # rows of so many heads lie head by head
+                            calls.append(_packed(n=n, m=n, b=b, h=h, kv=kv, dim=dim, dt=dt, qt=dim,
+                                                 qh=n * dim, kt=dim, kh=n * dim, vt=dim, vh=n * dim,
+                                                 ot=dim, oh=n * dim))
     for n in (1, 1000, INT32_MAX):
         for h in (1, 8, 65536):
             for dim in (32, 128):

@@ -153,11 +153,16 @@ struct TileLoad {
 
   __device__ __forceinline__ TileLoad(int wave, int lane, int64_t row_stride, int dim)
       : stride(row_stride) {
+    // row r0 + i STEP of load i; the key of a sum of disjoint bits is the exclusive
+    // or of their keys
+    constexpr int STEP = WAVES * kWave / L::C;
+    const int at = wave * kWave + lane, r0 = at / L::C;
+    const uint32_t place = at % L::C ^ L::key(r0 & 15);
+    const uint32_t row = (uint32_t)row_stride * (uint32_t)sizeof(S), at0 = r0 * row;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int at = (i * WAVES + wave) * kWave + lane, r = at / L::C;
-      const int c = ((at % L::C) ^ L::key(r & 15)) * L::E;
-      from[i] = c < dim ? ((uint32_t)r * (uint32_t)row_stride + c) * (uint32_t)sizeof(S) : kNowhere;
+      const uint32_t c = place ^ L::key(i * STEP & 15);
+      from[i] = c * L::E < (uint32_t)dim ? c * 16 + (at0 + i * STEP * row) : kNowhere;
     }
   }
   __device__ __forceinline__ void start(const S *base, int rows) {
@@ -207,8 +212,9 @@ struct MemoryRow {
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
-        const int c = d * 32 + row_of(i, half);
-        const uint32_t to = c < dim ? row + c * (uint32_t)sizeof(S) : kNowhere;
+        const int c = d * 32 + row_of(i, 0);   // (and four more for the other half: rows
+        const uint32_t to =                    // hold a multiple of eight)
+            c < dim ? row + (c + half * 4) * (uint32_t)sizeof(S) : kNowhere;
         const float w[4] = {o[d][i] * scale, o[d][i + 1] * scale, o[d][i + 2] * scale,
                             o[d][i + 3] * scale};
         if constexpr (sizeof(S) == 4)
@@ -443,6 +449,13 @@ __device__ __forceinline__ Item item_of(int64_t i, int64_t tiles, int heads) {
   }
   if (heads % 8 == 0) r = r % 8 * (heads / 8) + r / 8;
   return {(uint32_t)(tiles - 1 - t), (int)r};
+}
+
+// A scalar whose uses stay within the loop over items: what follows from it would
+// else be made before the loop and kept, beyond the registers that there are.
+__device__ __forceinline__ int in_loop(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
 }
 
 // Workgroups for that many items; each takes those a grid apart.

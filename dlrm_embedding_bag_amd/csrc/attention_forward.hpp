@@ -75,10 +75,11 @@ __device__ __forceinline__ void add_others(f32x16_t (&o)[DT], const typename T::
 // A lane's half of a row: its sums relative to m, l the row's whole.
 template <typename T, int DT>
 __device__ __forceinline__ void put_row(const AttentionParams &p, const f32x16_t (&o)[DT], float m,
-                                        float l, const Tile &t, int mine, int head, int half) {
+                                        float l, const Tile &t, int dim, int mine, int head,
+                                        int half) {
   using S = typename T::S;
   const MemoryRow<T> out((S *)p.out.data + t.row * p.out.token + head * p.out.head, p.out.token,
-                         t.left, p.dim, mine);
+                         t.left, dim, mine);
   out.store(o, l > 0.0f || l != l ? 1.0f / l : 0.0f, half);
   if (p.lse && half == 0 && mine < t.left)
     p.lse[((int64_t)t.row + mine) * p.heads + head] =

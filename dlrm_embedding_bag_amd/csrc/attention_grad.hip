@@ -68,6 +68,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
   const float c = p.scale * kLog2e;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int dim = in_loop(p.dim);
     const Item at = item_of(item, tile_count(p.tokens, p.batch, BM), p.heads);
     const int head = at.head;
     const Tile t = find_tile(p.offsets, p.batch, p.tokens, at.tile, BM);
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     if (t.sequence < 0) {
       if (there && half == 0 && p.fill & 1) {
         S *dq = (S *)p.dq.data + row * p.dq.token + head * p.dq.head;
-        for (int d = 0; d < p.dim; ++d) dq[d] = 0;
+        for (int d = 0; d < dim; ++d) dq[d] = 0;
       }
       continue;
     }
@@ -93,11 +94,11 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     float delta = 0.0f;
     {
       const MemoryRow<T> qs((const S *)p.q.data + t.row * p.q.token + head * p.q.head, p.q.token,
-                            t.left, p.dim, mine);
+                            t.left, dim, mine);
       const MemoryRow<T> gs((const S *)p.grad.data + t.row * p.grad.token + head * p.grad.head,
-                            p.grad.token, t.left, p.dim, mine);
+                            p.grad.token, t.left, dim, mine);
       const MemoryRow<T> os((const S *)p.out.data + t.row * p.out.token + head * p.out.head,
-                            p.out.token, t.left, p.dim, mine);
+                            p.out.token, t.left, dim, mine);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const int at = s * 16 + half * 8;
@@ -121,8 +122,8 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
     vload.start((const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head, keys.count);
     auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
-      kload.fill(k, p.dim, wave);
-      vload.fill(v, p.dim, wave);
+      kload.fill(k, dim, wave);
+      vload.fill(v, dim, wave);
     };
     auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       const int base = n * BN;
@@ -175,7 +176,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
       }
       landed();
     }
-    MemoryRow<T>((S *)p.dq.data + t.row * p.dq.token + head * p.dq.head, p.dq.token, t.left, p.dim,
+    MemoryRow<T>((S *)p.dq.data + t.row * p.dq.token + head * p.dq.head, p.dq.token, t.left, dim,
                  mine)
         .store(o, p.scale, half);
   }
@@ -228,6 +229,7 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
   const uint32_t by_stat = half * 16 + part * 2 * kWave * 4;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int dim = in_loop(p.dim);
     // (the first keys, which most rows see, come first)
     const int64_t tiles = tile_count(p.kv_tokens, p.batch, BM);
     const Item at = item_of(item, tiles, kv_heads);
@@ -240,7 +242,7 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
         const int64_t key = (int64_t)t.row + mine;
         S *dk = (S *)p.dk.data + key * p.dk.token + kv_head * p.dk.head;
         S *dv = (S *)p.dv.data + key * p.dv.token + kv_head * p.dv.head;
-        for (int d = 0; d < p.dim; ++d) {
+        for (int d = 0; d < dim; ++d) {
           if (p.fill & 2) dk[d] = 0;
           if (p.fill & 4) dv[d] = 0;
         }
@@ -267,9 +269,9 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
     Operand<T> k[STEPS], v[STEPS];
     {
       const MemoryRow<T> ks((const S *)p.k.data + t.row * p.k.token + kv_head * p.k.head, p.k.token,
-                            t.left, p.dim, mine);
+                            t.left, dim, mine);
       const MemoryRow<T> vs((const S *)p.v.data + t.row * p.v.token + kv_head * p.v.head, p.v.token,
-                            t.left, p.dim, mine);
+                            t.left, dim, mine);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         k[s] = ks.load(s * 16 + half * 8);
@@ -304,8 +306,8 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
       const int64_t head = (int64_t)kv_head * p.group + asked.head, row = (int64_t)rows.first + skip;
       qload.start((const S *)p.q.data + row * p.q.token + head * p.q.head, left);
       gload.start((const S *)p.grad.data + row * p.grad.token + head * p.grad.head, left);
-      qload.fill(q + part * L::SIZE, p.dim, wave);
-      gload.fill(g + part * L::SIZE, p.dim, wave);
+      qload.fill(q + part * L::SIZE, dim, wave);
+      gload.fill(g + part * L::SIZE, dim, wave);
       fill_stats<BN, WAVES>(st + part * 2 * kWave, stats, head * p.tokens + row, left, wave, lane);
       move(asked, GROUPS);
     };
@@ -411,10 +413,10 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
     }
     if (part == 0) {
       MemoryRow<T>((S *)p.dk.data + t.row * p.dk.token + kv_head * p.dk.head, p.dk.token, t.left,
-                   p.dim, mine)
+                   dim, mine)
           .store(ok, p.scale, half);
       MemoryRow<T>((S *)p.dv.data + t.row * p.dv.token + kv_head * p.dv.head, p.dv.token, t.left,
-                   p.dim, mine)
+                   dim, mine)
           .store(ov, 1.0f, half);
     }
   }

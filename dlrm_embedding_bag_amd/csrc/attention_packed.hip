@@ -39,6 +39,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
   const float c = p.scale * kLog2e;
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int dim = in_loop(p.dim);
     const Item at = item_of(item, tile_count(p.tokens, p.batch, BM), p.heads);
     const int head = at.head;
     const Tile t = find_tile(p.offsets, p.batch, p.tokens, at.tile, BM);
@@ -58,7 +59,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     Operand<T> q[STEPS];
     {
       const MemoryRow<T> from((const S *)p.q.data + t.row * p.q.token + head * p.q.head, p.q.token,
-                              t.left, p.dim, mine);
+                              t.left, dim, mine);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) q[s] = from.load(s * 16 + half * 8);
     }
@@ -71,8 +72,8 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
     vload.start(vbase, keys.count);
     auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
-      kload.fill(k, p.dim, wave);
-      vload.fill(v, p.dim, wave);
+      kload.fill(k, dim, wave);
+      vload.fill(v, dim, wave);
     };
     auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       const int base = n * BN;
@@ -162,9 +163,9 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     }
 
     if (loose >= 0)
-      add_others<T, DT>(o, vbase, p.v.token, p.dim, loose * BN, seen.wave_any, seen_keys, half);
+      add_others<T, DT>(o, vbase, p.v.token, dim, loose * BN, seen.wave_any, seen_keys, half);
     l += __uint_as_float(lane_xor<32>(__float_as_uint(l)));
-    put_row<T, DT>(p, o, m, l, t, mine, head, half);
+    put_row<T, DT>(p, o, m, l, t, dim, mine, head, half);
   }
 }
 

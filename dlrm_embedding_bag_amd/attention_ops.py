@@ -324,26 +324,32 @@ def kv_cache(pages, page, heads, dim, bits=8, device=None):
 
 def _cache(torch, cache, dev):
     """pages, page, bits and pointers of a cache, its heads and dim."""
-    codes, scales = cache[0], cache[1]
-    for i, t in enumerate(cache):
-        what = KVCache._fields[i]
-        _on(torch, t, what, dev)
-        if t.dtype is not torch.uint8:
-            raise TypeError(f"{what} must be torch.uint8 (got {t.dtype})")
-        if t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous (pages, heads, page, bytes)")
-    if codes.shape != cache[2].shape or scales.shape != cache[3].shape or (
-            codes.shape[:3] != scales.shape[:3]):
+    kc, ks, vc, vs = cache
+    u8 = torch.uint8
+    for i, t in enumerate((kc, ks, vc, vs)):
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+            _on(torch, t, KVCache._fields[i], dev)
+        if t.dtype is not u8:
+            raise TypeError(f"{KVCache._fields[i]} must be torch.uint8 (got {t.dtype})")
+        if not t.is_contiguous():
+            raise ValueError(f"{KVCache._fields[i]} must be contiguous (pages, heads, page, bytes)")
+    codes, scales = kc.shape, ks.shape
+    if len(codes) != 4 or len(scales) != 4:
+        raise ValueError("codes and scales must be (pages, heads, page, bytes)")
+    pages, heads, page, row = codes
+    if vc.shape != codes or vs.shape != scales or scales != (pages, heads, page, scales[3]):
         raise ValueError("codes and scales of keys and values must have the same pages, heads, "
                          "page and dim")
-    pages, heads, page, row = codes.shape
-    dim = scales.shape[3] * 32
-    if not dim or row * 8 % dim or row * 8 // dim not in (4, 8):
+    dim = scales[3] * 32
+    if row == dim and dim:
+        bits = 8
+    elif row * 2 == dim and dim:
+        bits = 4
+    else:
         raise ValueError("codes must have 32 or 16 bytes for each byte of the scales")
     if pages > _INT_MAX or heads > _INT_MAX or page > _INT_MAX or dim > _INT_MAX:
         raise ValueError(f"the cache has a dimension above {_INT_MAX}")
-    return (pages, page, row * 8 // dim, codes.data_ptr(), scales.data_ptr(), cache[2].data_ptr(),
-            cache[3].data_ptr()), heads, dim
+    return (pages, page, bits, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()), heads, dim
 
 
 def kv_cache_write(cache, k, v, slots, stream=None):

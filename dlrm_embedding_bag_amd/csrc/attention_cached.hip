@@ -381,15 +381,16 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(CachedParams p, int 
 
 int head_tiles_of(int group) { return (group + kHeads - 1) / kHeads; }
 
-// Shares of a sequence: enough workgroups to fill the card several times over,
-// none with less than a step for each of its waves.
+// Shares of a sequence: two workgroups a CU (one sequence of 131001 keys, 8 key heads
+// of 128 in 4 bits: 64 shares 35 us, 32 43, 128 42), or where sequences are many,
+// four shares each, since the long ones among them would end last; none with less
+// than a step for each of its waves.
 int splits_of(int64_t batch, int heads, int kv_heads, int64_t max_pages, int page) {
   const int64_t groups = batch * kv_heads * head_tiles_of(heads / kv_heads);
-  const int64_t longest = max_pages * page;
-  const int64_t most = (longest + kWaves * kStep - 1) / (kWaves * kStep);
-  int64_t want = (2048 + groups - 1) / groups;
+  const int64_t most = (max_pages * page + kWaves * kStep - 1) / (kWaves * kStep);
+  int64_t want = (512 + groups - 1) / groups;
+  want = want < 4 ? 4 : want > 256 ? 256 : want;
   want = want < most ? want : most;
-  want = want < 128 ? want : 128;
   return want < 1 ? 1 : (int)want;
 }
 

@@ -304,7 +304,8 @@ struct ReadColumns {
 };
 
 // Waves of a SIMD that a kernel leaves registers for: two cover each other's waits,
-// but float32 rows of more than 64 would spill (XX).
+// but float32 rows of more than 64 would spill (gradient of 2 x 2000 rows, 8 heads of
+// 128: one wave 1361 us, two 1892).
 template <typename T, int DP>
 constexpr int waves_a_simd = sizeof(typename T::S) == 4 && DP > 64 ? 1 : 2;
 

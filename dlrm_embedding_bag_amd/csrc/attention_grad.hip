@@ -441,7 +441,8 @@ hipError_t run_keys(const AttentionGradParams &p, float *ws, hipStream_t stream)
 
 // Sequences of few rows take a wave each, and none waits for another (64 of 100
 // rows, 8 heads of 64: 35 us for 40).  Else a workgroup takes 128 rows or keys, but
-// 64 keys where that would leave CUs without one (2000 keys of two key heads: XX).
+// 64 keys where that would leave CUs without one (2 x 2000 rows, two key heads of
+// 128: 210 us for 261).
 template <typename T, int DP>
 hipError_t run(const AttentionGradParams &p, float *ws, hipStream_t stream) {
   constexpr int BN = sizeof(typename T::S) == 4 ? 32 : 64;

@@ -307,7 +307,7 @@ __global__ __launch_bounds__(kSumThreads) void rope_weight_kernel(const float *p
   if (g == 0 && i < dim) out[i] = (float)part[0][e];
 }
 
-constexpr int kGradBlocks = 1024;   // four a CU
+constexpr int kGradBlocks = 512;   // two a CU
 constexpr int kBlockTokens = 4;
 
 // Several tokens a workgroup share the heads evenly over its lanes; few tokens

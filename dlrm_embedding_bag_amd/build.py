@@ -14,10 +14,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdlrm_mi355x.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["abi.hip", "attention_abi.hip", "attention_cached.hip", "attention_grad.hip",
-           "attention_packed.hip", "bottom_mlp.hip", "emb_interact.hip", "forward_small.hip",
-           "kv_cache.hip", "linear.hip",
-           "linear_i8.hip", "mlp_chain.hip", "probe.hip", "qk_norm_rope.hip", "rms_norm_i8.hip", "slice_mlp.hip",
-           "token_abi.hip", "token_grad.hip", "token_lookup.hip"]
+           "attention_packed.hip", "attention_short.hip", "bottom_mlp.hip", "emb_interact.hip",
+           "forward_small.hip", "kv_cache.hip", "linear.hip", "linear_i8.hip",
+           "mlp_chain.hip", "probe.hip", "qk_norm_rope.hip", "rms_norm_i8.hip",
+           "slice_mlp.hip", "token_abi.hip", "token_grad.hip", "token_lookup.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

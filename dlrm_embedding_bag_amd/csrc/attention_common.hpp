@@ -459,6 +459,19 @@ __device__ __forceinline__ int in_loop(int v) {
   return v;
 }
 
+// What the gradient's second kernel needs of a row, head by head in planes of `tokens`: lse in
+// units of log 2, +inf where the row sees nothing, with the bits of +inf turned so
+// that the zeros that are read behind the last row stand for it, too; and -delta.
+constexpr uint32_t kInfinity = 0x7f800000u;
+struct Stats {
+  float *turned_lse2, *minus_delta;
+  __host__ __device__ Stats(float *at, int64_t tokens, int64_t heads)
+      : turned_lse2(at), minus_delta(at + tokens * heads) {}
+};
+__device__ __forceinline__ float turned(float lse2) {
+  return __uint_as_float(__float_as_uint(lse2) ^ kInfinity);
+}
+
 // Workgroups for that many items; each takes those a grid apart.
 inline uint32_t grid_of(int64_t items) {
   return (uint32_t)(items < (1 << 22) ? items : 1 << 22);

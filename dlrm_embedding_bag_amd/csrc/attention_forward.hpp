@@ -18,6 +18,13 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
                                     : ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
 }
 
+template <typename T>
+__device__ __forceinline__ uint32_t finite(uint32_t w) {   // zeros in their place
+  const uint32_t n = not_finite<T>(w);
+  // a sign bit to all bits of its element
+  return w & ~(sizeof(typename T::S) == 4 ? (n ? 0xffffffffu : 0u) : (n >> 15) * 0xffffu);
+}
+
 // A tile of values in LDS: whether it holds one that is not finite, for all
 // waves; if so it is zero there when this returns.
 template <typename T, int SIZE, int WAVES>
@@ -41,11 +48,7 @@ __device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int lan
     LdsChunks at = v + (i * WAVES + wave) * kWave + lane;
     u32x4_t w = *at;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t n = not_finite<T>(w[e]);
-      // a sign bit to all bits of its element
-      w[e] &= ~(sizeof(typename T::S) == 4 ? (n ? 0xffffffffu : 0u) : (n >> 15) * 0xffffu);
-    }
+    for (int e = 0; e < 4; ++e) w[e] = finite<T>(w[e]);
     *at = w;
   }
   landed();
@@ -72,6 +75,11 @@ __device__ __forceinline__ void add_others(f32x16_t (&o)[DT], const typename T::
   }
 }
 
+// The logarithm of a row's whole, l relative to m.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
+}
+
 // A lane's half of a row: its sums relative to m, l the row's whole.
 template <typename T, int DT>
 __device__ __forceinline__ void put_row(const AttentionParams &p, const f32x16_t (&o)[DT], float m,
@@ -82,8 +90,7 @@ __device__ __forceinline__ void put_row(const AttentionParams &p, const f32x16_t
                          t.left, dim, mine);
   out.store(o, l > 0.0f || l != l ? 1.0f / l : 0.0f, half);
   if (p.lse && half == 0 && mine < t.left)
-    p.lse[((int64_t)t.row + mine) * p.heads + head] =
-        l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
+    p.lse[((int64_t)t.row + mine) * p.heads + head] = lse_of(m, l);
 }
 
 // A row outside all sequences.

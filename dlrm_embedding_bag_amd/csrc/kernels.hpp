@@ -323,6 +323,8 @@ struct AttentionParams {
   float *lse;      // (tokens, heads), or null
 };
 hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream);
+// The same, for sequences of few rows (attention_short.hip).
+hipError_t launch_attention_short(const AttentionParams &p, int dtype, hipStream_t stream);
 
 struct AttentionGradParams {
   int64_t tokens, kv_tokens, batch;
@@ -338,6 +340,8 @@ struct AttentionGradParams {
 size_t attention_grad_workspace(int64_t tokens, int heads);
 hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *ws,
                                  hipStream_t stream);
+hipError_t launch_attention_grad_short(const AttentionGradParams &p, int dtype, void *ws,
+                                       hipStream_t stream);
 
 // Paged cache in 8 or 4 bits (kv_cache.hip): codes (pages, heads, page, dim *
 // bits / 8), scales (pages, heads, page, dim / 32).

@@ -175,8 +175,40 @@ struct TileLoad {
     const auto b = buffer_of(next, ((rows - 1) * (uint32_t)stride + dim) * (uint32_t)sizeof(S));
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load_to_lds(b, from[i], lds + (i * WAVES + wave) * kWave);
-    next += ROWS * stride;
-    left -= ROWS;
+    skip(ROWS);
+  }
+  __device__ __forceinline__ void skip(int rows) {
+    next += rows * stride;
+    left -= rows;
+  }
+};
+
+// Where two groups of WAVES waves that share their rows or keys meet at the end: the
+// four buffers of their tiles (SIZE chunks each for a group) take 16 sums of each lane
+// at a time.
+template <int WAVES, int SIZE>
+struct Meeting {
+  static constexpr int EACH = 2 * SIZE * 16 / (WAVES * kWave * 64);   // of a buffer
+  static_assert(EACH >= 1);
+  LdsChunks buffers[4];
+  int at;
+  __device__ __forceinline__ LdsChunks place(int i, int e) const {
+    return buffers[i / EACH] + (i % EACH * 4 + e) * WAVES * kWave + at;
+  }
+  __device__ __forceinline__ void put(int i, const f32x16_t &a) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *place(i, e) = u32x4_t{__float_as_uint(a[4 * e]), __float_as_uint(a[4 * e + 1]),
+                             __float_as_uint(a[4 * e + 2]), __float_as_uint(a[4 * e + 3])};
+  }
+  __device__ __forceinline__ void add(int i, f32x16_t &a, float scale = 1.0f) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const u32x4_t w = *place(i, e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        a[4 * e + j] = __builtin_fmaf(__uint_as_float(w[j]), scale, a[4 * e + j]);
+    }
   }
 };
 
@@ -470,6 +502,16 @@ struct Stats {
 };
 __device__ __forceinline__ float turned(float lse2) {
   return __uint_as_float(__float_as_uint(lse2) ^ kInfinity);
+}
+
+// Whether workgroups of 128 rows would leave CUs without one, or in float32, which
+// the matrix cores bound, with one more than others: then two groups of waves share
+// the keys of 64 rows.  (One sequence of 1466 keys, 8 heads of 96 in float32 93 us for
+// 155, in bfloat16 25 for 29; of 2 x 2000 rows, 16 heads of 128, which 400 workgroups
+// hold, 302 for 438 and 80 for 59.)
+template <typename T>
+inline bool few_tiles(int64_t tokens, int heads) {
+  return tokens / 128 * heads < (sizeof(typename T::S) == 4 ? 512 : 256);
 }
 
 // Workgroups for that many items; each takes those a grid apart.

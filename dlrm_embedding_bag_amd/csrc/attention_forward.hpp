@@ -25,10 +25,10 @@ __device__ __forceinline__ uint32_t finite(uint32_t w) {   // zeros in their pla
   return w & ~(sizeof(typename T::S) == 4 ? (n ? 0xffffffffu : 0u) : (n >> 15) * 0xffffu);
 }
 
-// A tile of values in LDS: whether it holds one that is not finite, for all
-// waves; if so it is zero there when this returns.
-template <typename T, int SIZE, int WAVES>
-__device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int lane) {
+// A tile of values in LDS for each group of WAVES waves: whether one holds a value
+// that is not finite, for all waves; if so it is zero there when this returns.
+template <typename T, int SIZE, int WAVES, int GROUPS>
+__device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int part, int lane) {
   constexpr int EACH = SIZE / (WAVES * kWave);
   uint32_t others = 0;
 #pragma unroll
@@ -38,11 +38,11 @@ __device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int lan
     for (int e = 0; e < 4; ++e) others |= not_finite<T>(w[e]);
   }
   const bool mine = __any(others != 0);
-  if (lane == 0) found[wave] = mine;
+  if (lane == 0) found[part * WAVES + wave] = mine;
   landed();
   bool any = false;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) any |= found[w] != 0;
+  for (int w = 0; w < WAVES * GROUPS; ++w) any |= found[w] != 0;
   if (!uniform((int)any)) return false;
   for (int i = 0; i < EACH; ++i) {
     LdsChunks at = v + (i * WAVES + wave) * kWave + lane;

@@ -36,18 +36,23 @@ __device__ __forceinline__ float dot(const Operand<T> &a, const Operand<T> &b, f
   return sum;
 }
 
-// Rows: dq, and the rows' statistics.
-template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows_kernel(AttentionGradParams p,
+// Rows: dq, and the rows' statistics.  GROUPS groups of WAVES waves hold the same rows
+// and take every GROUPS-th tile of keys, as in the forward pass.
+template <typename T, int DP, int WAVES, int BN, int GROUPS>
+__global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void grad_rows_kernel(AttentionGradParams p,
                                                                  float *ws, int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
   constexpr int AHEAD = sizeof(S) == 2 ? 4 : 2;
   constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
-  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
+  __shared__ u32x4_t k0s[GROUPS * L::SIZE], v0s[GROUPS * L::SIZE];
+  __shared__ u32x4_t k1s[GROUPS * SECOND], v1s[GROUPS * SECOND];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int part = GROUPS > 1 ? wave_of_all / WAVES : 0, wave = wave_of_all - part * WAVES;
+  const LdsChunks k0 = (LdsChunks)k0s + part * L::SIZE, v0 = (LdsChunks)v0s + part * L::SIZE;
+  const LdsChunks k1 = (LdsChunks)k1s + part * L::SIZE, v1 = (LdsChunks)v1s + part * L::SIZE;
   TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
   TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
   const ReadRows<T, BN, DP> by_row(lane);
@@ -64,7 +69,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     const int64_t row = (int64_t)t.row + mine;
     const bool there = mine < t.left;
     if (t.sequence < 0) {
-      if (there && half == 0 && p.fill & 1) {
+      if (there && half == 0 && part == 0 && p.fill & 1) {
         S *dq = (S *)p.dq.data + row * p.dq.token + head * p.dq.head;
         for (int d = 0; d < dim; ++d) dq[d] = 0;
       }
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     delta += __uint_as_float(lane_xor<32>(__float_as_uint(delta)));
     float lse2 = there ? p.lse[row * p.heads + head] * kLog2e : INFINITY;
     if (lse2 == -INFINITY) lse2 = INFINITY;
-    if (there && half == 0) {
+    if (there && half == 0 && part == 0) {
       const Stats stats(ws, p.tokens, p.heads);
       stats.turned_lse2[head * p.tokens + row] = turned(lse2);
       stats.minus_delta[head * p.tokens + row] = -delta;
@@ -108,12 +113,18 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
     kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
     vload.start((const S *)p.v.data + keys.first * p.v.token + kv_head * p.v.head, keys.count);
+    kload.skip(part * BN);
+    vload.skip(part * BN);
+    const int rounds = count / GROUPS + (count % GROUPS != 0);
     auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
+      if (GROUPS > 1 && kload.left <= 0) return;
       kload.fill(k, dim, wave);
       vload.fill(v, dim, wave);
+      kload.skip((GROUPS - 1) * BN);
+      vload.skip((GROUPS - 1) * BN);
     };
     auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
-      const int base = n * BN;
+      const int base = (n * GROUPS + part) * BN;
       if (base >= seen.wave_any) return;
       const bool masked = seen.wave_all - base < BN;
       const int left = seen_keys - base - half * 4;
@@ -143,25 +154,40 @@ __global__ __launch_bounds__(WAVES *kWave, (waves_a_simd<T, DP>)) void grad_rows
       }
     };
     if constexpr (WAVES == 1) {
-      for (int n = 0; n < count; ++n) {
-        fill((LdsChunks)k0, (LdsChunks)v0);
+      for (int n = 0; n < rounds; ++n) {
+        fill(k0, v0);
         landed();
-        work((LdsChunks)k0, (LdsChunks)v0, n);
+        work(k0, v0, n);
         landed();
       }
     } else {
-      if (count > 0) fill((LdsChunks)k0, (LdsChunks)v0);
-      for (int n = 0; n < count; n += 2) {
+      if (rounds > 0) fill(k0, v0);
+      for (int n = 0; n < rounds; n += 2) {
         landed();
-        if (n + 1 < count) fill((LdsChunks)k1, (LdsChunks)v1);
-        work((LdsChunks)k0, (LdsChunks)v0, n);
-        if (n + 1 < count) {
+        if (n + 1 < rounds) fill(k1, v1);
+        work(k0, v0, n);
+        if (n + 1 < rounds) {
           landed();
-          if (n + 2 < count) fill((LdsChunks)k0, (LdsChunks)v0);
-          work((LdsChunks)k1, (LdsChunks)v1, n + 1);
+          if (n + 2 < rounds) fill(k0, v0);
+          work(k1, v1, n + 1);
         }
       }
       landed();
+    }
+    if constexpr (GROUPS == 2) {
+      const Meeting<WAVES, L::SIZE> meeting{
+          {(LdsChunks)k0s, (LdsChunks)v0s, (LdsChunks)k1s, (LdsChunks)v1s}, wave * kWave + lane};
+      if (part == 1) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) meeting.put(d, o[d]);
+      }
+      landed();
+      if (part == 0) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) meeting.add(d, o[d]);
+      }
+      landed();
+      if (part == 1) continue;
     }
     MemoryRow<T>((S *)p.dq.data + t.row * p.dq.token + head * p.dq.head, p.dq.token, t.left, dim,
                  mine)
@@ -198,7 +224,7 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
   __shared__ float s0s[GROUPS * 2 * kWave], s1s[GROUPS * 2 * kWave];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
   const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wave = wave_of_all % WAVES, part = wave_of_all / WAVES;
+  const int part = GROUPS > 1 ? wave_of_all / WAVES : 0, wave = wave_of_all - part * WAVES;
   const LdsChunks q0 = (LdsChunks)q0s, g0 = (LdsChunks)g0s, q1 = (LdsChunks)q1s,
                   g1 = (LdsChunks)g1s;
   const LdsFloats s0 = (LdsFloats)s0s, s1 = (LdsFloats)s1s;
@@ -367,34 +393,23 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
       landed();
     }
     if constexpr (GROUPS == 2) {
-      // the second group's sums, 16 of a lane at a time, wherever a tile was
-      constexpr int EACH = GROUPS * L::SIZE * 16 / (WAVES * kWave * 64);   // of a buffer
-      static_assert(EACH >= 1 && EACH * 4 >= 2 * DT);
-      const LdsChunks buffers[4] = {(LdsChunks)q0s, (LdsChunks)g0s, (LdsChunks)q1s, (LdsChunks)g1s};
-      auto place = [&](int i, int e) {
-        return buffers[i / EACH] + (i % EACH * 4 + e) * WAVES * kWave + wave * kWave + lane;
-      };
+      static_assert(Meeting<WAVES, L::SIZE>::EACH * 4 >= 2 * DT);
+      const Meeting<WAVES, L::SIZE> meeting{
+          {(LdsChunks)q0s, (LdsChunks)g0s, (LdsChunks)q1s, (LdsChunks)g1s}, wave * kWave + lane};
       if (part == 1) {
 #pragma unroll
-        for (int i = 0; i < 2 * DT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const f32x16_t &a = i < DT ? ok[i] : ov[i - DT];
-            *place(i, e) = u32x4_t{__float_as_uint(a[4 * e]), __float_as_uint(a[4 * e + 1]),
-                                   __float_as_uint(a[4 * e + 2]), __float_as_uint(a[4 * e + 3])};
-          }
+        for (int d = 0; d < DT; ++d) {
+          meeting.put(d, ok[d]);
+          meeting.put(DT + d, ov[d]);
+        }
       }
       landed();
       if (part == 0) {
 #pragma unroll
-        for (int i = 0; i < 2 * DT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const u32x4_t w = *place(i, e);
-            f32x16_t &a = i < DT ? ok[i] : ov[i - DT];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[4 * e + j] += __uint_as_float(w[j]);
-          }
+        for (int d = 0; d < DT; ++d) {
+          meeting.add(d, ok[d]);
+          meeting.add(DT + d, ov[d]);
+        }
       }
       landed();   // the buffers are free for the next item
     }
@@ -409,11 +424,11 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, (waves_a_simd<T, DP>)) void g
   }
 }
 
-template <typename T, int DP, int WAVES, int BN>
+template <typename T, int DP, int WAVES, int BN, int GROUPS>
 hipError_t run_rows(const AttentionGradParams &p, float *ws, hipStream_t stream) {
   const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
-  launch_kernel(grad_rows_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), dim3(WAVES * kWave), 0,
-                stream, p, ws, items);
+  launch_kernel(grad_rows_kernel<T, DP, WAVES, BN, GROUPS>, dim3(grid_of(items)),
+                dim3(WAVES * GROUPS * kWave), 0, stream, p, ws, items);
   return hipGetLastError();
 }
 
@@ -435,8 +450,10 @@ hipError_t run(const AttentionGradParams &p, float *ws, hipStream_t stream) {
   constexpr int BN = sizeof(typename T::S) == 4 ? 32 : 64;
   const bool few = (p.tokens > p.kv_tokens ? p.tokens : p.kv_tokens) / p.batch <= 128;
   if (p.tokens) {
-    const hipError_t e =
-        few ? run_rows<T, DP, 1, 32>(p, ws, stream) : run_rows<T, DP, 4, BN>(p, ws, stream);
+    const hipError_t e = few ? run_rows<T, DP, 1, 32, 1>(p, ws, stream)
+                         : few_tiles<T>(p.tokens, p.heads)
+                             ? run_rows<T, DP, 2, BN, 2>(p, ws, stream)
+                             : run_rows<T, DP, 4, BN, 1>(p, ws, stream);
     if (e != hipSuccess) return e;
   }
   if (!p.kv_tokens) return hipSuccess;
@@ -445,7 +462,8 @@ hipError_t run(const AttentionGradParams &p, float *ws, hipStream_t stream) {
   if constexpr (DP == 32) {
     return run_keys<T, DP, 4, BN, 1>(p, ws, stream);
   } else {
-    if (sizeof(typename T::S) == 2 && wide >= 256) return run_keys<T, DP, 4, BN, 2>(p, ws, stream);
+    if constexpr (sizeof(typename T::S) == 2)
+      if (wide >= 256) return run_keys<T, DP, 4, BN, 2>(p, ws, stream);
     return run_keys<T, DP, 2, BN, 2>(p, ws, stream);
   }
 }

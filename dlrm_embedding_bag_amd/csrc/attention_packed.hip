@@ -20,18 +20,25 @@
 namespace dlrm {
 namespace {
 
-template <typename T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionParams p,
-                                                                 int64_t items) {
+// GROUPS groups of WAVES waves hold the same rows and take every GROUPS-th tile of keys,
+// each from buffers of its own; their sums meet in LDS at the end.
+template <typename T, int DP, int WAVES, int BN, int GROUPS>
+__global__ __launch_bounds__(WAVES *GROUPS *kWave, 2) void attention_kernel(AttentionParams p,
+                                                                         int64_t items) {
   using S = typename T::S;
   using L = LdsTile<T, BN, DP>;
   constexpr int BM = WAVES * 32, KT = BN / 32, STEPS = DP / 16, DT = DP / 32;
   constexpr int AHEAD = sizeof(S) == 2 ? 4 : 2;
   constexpr int SECOND = WAVES > 1 ? L::SIZE : 1;   // a lone wave has one buffer
-  __shared__ u32x4_t k0[L::SIZE], v0[L::SIZE], k1[SECOND], v1[SECOND];
-  __shared__ int found[WAVES];
+  __shared__ u32x4_t k0s[GROUPS * L::SIZE], v0s[GROUPS * L::SIZE];
+  __shared__ u32x4_t k1s[GROUPS * SECOND], v1s[GROUPS * SECOND];
+  __shared__ int found[WAVES * GROUPS];
+  __shared__ float whole[GROUPS > 1 ? 2 * WAVES * kWave : 1];
   const int lane = threadIdx.x % kWave, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int part = GROUPS > 1 ? wave_of_all / WAVES : 0, wave = wave_of_all - part * WAVES;
+  const LdsChunks k0 = (LdsChunks)k0s + part * L::SIZE, v0 = (LdsChunks)v0s + part * L::SIZE;
+  const LdsChunks k1 = (LdsChunks)k1s + part * L::SIZE, v1 = (LdsChunks)v1s + part * L::SIZE;
   TileLoad<T, BN, DP, WAVES> kload(wave, lane, p.k.token, p.dim);
   TileLoad<T, BN, DP, WAVES> vload(wave, lane, p.v.token, p.dim);
   const ReadRows<T, BN, DP> by_row(lane);
@@ -46,7 +53,7 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // row of the tile
     if (t.sequence < 0) {
-      if (mine < t.left && half == 0) put_nothing<T>(p, (int64_t)t.row + mine, head);
+      if (mine < t.left && half == 0 && part == 0) put_nothing<T>(p, (int64_t)t.row + mine, head);
       continue;
     }
     const Range keys = p.kv_offsets ? rows_of(p.kv_offsets, p.batch, p.kv_tokens, t.sequence)
@@ -67,16 +74,22 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
     float m = -INFINITY, l = 0.0f;
-    int loose = -1;   // the first tile whose values are not all added
+    int loose = -1;   // the first round of tiles whose values are not all added
 
     kload.start((const S *)p.k.data + keys.first * p.k.token + kv_head * p.k.head, keys.count);
     vload.start(vbase, keys.count);
+    kload.skip(part * BN);
+    vload.skip(part * BN);
+    const int rounds = count / GROUPS + (count % GROUPS != 0);
     auto fill = [&](LdsChunks k, LdsChunks v) __attribute__((always_inline)) {
+      if (GROUPS > 1 && kload.left <= 0) return;
       kload.fill(k, dim, wave);
       vload.fill(v, dim, wave);
+      kload.skip((GROUPS - 1) * BN);
+      vload.skip((GROUPS - 1) * BN);
     };
     auto work = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
-      const int base = n * BN;
+      const int base = (n * GROUPS + part) * BN;
       if (base >= seen.wave_any) return;
       const bool masked = seen.wave_all - base < BN;
       f32x16_t s[KT];
@@ -134,69 +147,98 @@ __global__ __launch_bounds__(WAVES *kWave, 2) void attention_kernel(AttentionPar
     // A value that is not finite must not reach the rows that do not see it, and
     // zero times it is not zero: from the first tile on that some row does not see
     // whole, such values are left out, and added after the last tile.
-    auto tile_of = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
-      if (p.causal && seen.tile_all - n * BN < BN && clean<T, L::SIZE, WAVES>(v, found, wave, lane))
+    auto round_of = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
+      if (p.causal && seen.tile_all - n * GROUPS * BN < GROUPS * BN &&
+          clean<T, L::SIZE, WAVES, GROUPS>(v, found, wave, part, lane))
         loose = loose < 0 ? n : loose;
       work(k, v, n);
     };
 
     if constexpr (WAVES == 1) {
-      for (int n = 0; n < count; ++n) {
-        fill((LdsChunks)k0, (LdsChunks)v0);
+      for (int n = 0; n < rounds; ++n) {
+        fill(k0, v0);
         landed();
-        tile_of((LdsChunks)k0, (LdsChunks)v0, n);
+        round_of(k0, v0, n);
         landed();
       }
     } else {
-      if (count > 0) fill((LdsChunks)k0, (LdsChunks)v0);
-      for (int n = 0; n < count; n += 2) {
+      if (rounds > 0) fill(k0, v0);
+      for (int n = 0; n < rounds; n += 2) {
         landed();
-        if (n + 1 < count) fill((LdsChunks)k1, (LdsChunks)v1);
-        tile_of((LdsChunks)k0, (LdsChunks)v0, n);
-        if (n + 1 < count) {
+        if (n + 1 < rounds) fill(k1, v1);
+        round_of(k0, v0, n);
+        if (n + 1 < rounds) {
           landed();
-          if (n + 2 < count) fill((LdsChunks)k0, (LdsChunks)v0);
-          tile_of((LdsChunks)k1, (LdsChunks)v1, n + 1);
+          if (n + 2 < rounds) fill(k0, v0);
+          round_of(k1, v1, n + 1);
         }
       }
       landed();  // nobody reads the tiles any more
     }
+    if constexpr (GROUPS == 2) {
+      const Meeting<WAVES, L::SIZE> meeting{
+          {(LdsChunks)k0s, (LdsChunks)v0s, (LdsChunks)k1s, (LdsChunks)v1s}, wave * kWave + lane};
+      float *const with = whole + 2 * (wave * kWave + lane);
+      if (part == 1) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) meeting.put(d, o[d]);
+        with[0] = m;
+        with[1] = l;
+      }
+      landed();
+      if (part == 0) {
+        const float other = with[0], next = fmaxf(m, other);
+        const float from = next == -INFINITY ? 0.0f : next;
+        const float mine_by = __builtin_amdgcn_exp2f(m - from);
+        const float other_by = __builtin_amdgcn_exp2f(other - from);
+        l = l * mine_by + with[1] * other_by;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          o[d] *= mine_by;
+          meeting.add(d, o[d], other_by);
+        }
+        m = next;
+      }
+      landed();   // the buffers are free for the next item
+      if (part == 1) continue;
+    }
 
     if (loose >= 0)
-      add_others<T, DT>(o, vbase, p.v.token, dim, loose * BN, seen.wave_any, seen_keys, half);
+      add_others<T, DT>(o, vbase, p.v.token, dim, loose * GROUPS * BN, seen.wave_any, seen_keys, half);
     l += __uint_as_float(lane_xor<32>(__float_as_uint(l)));
     put_row<T, DT>(p, o, m, l, t, dim, mine, head, half);
   }
 }
 
-template <typename T, int DP, int WAVES, int BN>
+template <typename T, int DP, int WAVES, int BN, int GROUPS>
 hipError_t run(const AttentionParams &p, hipStream_t stream) {
   const int64_t items = tile_count(p.tokens, p.batch, WAVES * 32) * p.heads;
-  launch_kernel(attention_kernel<T, DP, WAVES, BN>, dim3(grid_of(items)), dim3(WAVES * kWave), 0,
-                stream, p, items);
+  launch_kernel(attention_kernel<T, DP, WAVES, BN, GROUPS>, dim3(grid_of(items)),
+                dim3(WAVES * GROUPS * kWave), 0, stream, p, items);
   return hipGetLastError();
 }
 
-template <typename T, int WAVES, int BN>
+template <typename T, int WAVES, int BN, int GROUPS>
 hipError_t by_dim(const AttentionParams &p, hipStream_t stream) {
-  if (p.dim <= 32) return run<T, 32, WAVES, BN>(p, stream);
-  if (p.dim <= 64) return run<T, 64, WAVES, BN>(p, stream);
-  if (p.dim <= 96) return run<T, 96, WAVES, BN>(p, stream);
-  return run<T, 128, WAVES, BN>(p, stream);
+  if (p.dim <= 32) return run<T, 32, WAVES, BN, GROUPS>(p, stream);
+  if (p.dim <= 64) return run<T, 64, WAVES, BN, GROUPS>(p, stream);
+  if (p.dim <= 96) return run<T, 96, WAVES, BN, GROUPS>(p, stream);
+  return run<T, 128, WAVES, BN, GROUPS>(p, stream);
+}
+
+// Sequences of few rows take a wave each, and none waits for another (64 of 100 rows,
+// 8 heads of 64: 12 us for 17 in bfloat16, 23 for 38 in float32); else four waves.
+template <typename T, int BN>
+hipError_t by_size(const AttentionParams &p, hipStream_t stream) {
+  if (p.tokens / p.batch <= 128) return by_dim<T, 1, 32, 1>(p, stream);
+  if (few_tiles<T>(p.tokens, p.heads)) return by_dim<T, 2, BN, 2>(p, stream);
+  return by_dim<T, 4, BN, 1>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream) {
-  // sequences of few rows take a wave each, and none waits for another
-  // (64 of 100 rows, 8 heads of 64: 12 us for 17 in bfloat16, 23 for 38 in float32)
-  // tiles of 16 rows for sequences of few (8 heads, the mean of their rows: in float32
-  // of 64 elements 10 42 us for 83, 40 26 for 35; in bfloat16 of 128 10 54 for 80, 40 23
-  // for 27, 64 44 for 36 with two waves a SIMD)
-  if (p.tokens / p.batch <= 40) return launch_attention_short(p, dtype, stream);
-  const bool few = p.tokens / p.batch <= 128;
-  if (dtype == kF32) return few ? by_dim<F32, 1, 32>(p, stream) : by_dim<F32, 4, 32>(p, stream);
-  return few ? by_dim<BF16, 1, 32>(p, stream) : by_dim<BF16, 4, 64>(p, stream);
+  return dtype == kF32 ? by_size<F32, 32>(p, stream) : by_size<BF16, 64>(p, stream);
 }
 
 }  // namespace dlrm

@@ -491,9 +491,10 @@ __device__ __forceinline__ int in_loop(int v) {
   return v;
 }
 
-// What the gradient's second kernel needs of a row, head by head in planes of `tokens`: lse in
-// units of log 2, +inf where the row sees nothing, with the bits of +inf turned so
-// that the zeros that are read behind the last row stand for it, too; and -delta.
+// What the gradient's second kernel needs of a row, head by head in planes of
+// `tokens`: lse in units of log 2, +inf where the row sees nothing, with the bits of
+// +inf turned so that the zeros that are read behind the last row stand for it, too;
+// and -delta.
 constexpr uint32_t kInfinity = 0x7f800000u;
 struct Stats {
   float *turned_lse2, *minus_delta;

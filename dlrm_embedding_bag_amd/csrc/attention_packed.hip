@@ -10,9 +10,11 @@
 // the operand of out^T += v^T p^T without leaving the registers; keys and values
 // pass through LDS, the next tile on its way while one is worked on.
 //
-// The scores' tile of 32 x 32 takes as long on the matrix cores (2 dim products
-// of 32 x 32) as its exponentials on the vector units at dim 128, so two waves a
-// SIMD cover each other.
+// In bfloat16 of 128 elements a tile's products, its exponentials and its reads of LDS
+// take about as long as each other, so two waves a SIMD cover each other.  (Four
+// prompts of up to 6500 rows, 32 heads: 800 us, 1000 TFLOP/s; a single wave a SIMD with
+// 64 rows, which halves the reads, 1207.  In float32 four of up to 3000 rows 117 TFLOP/s of
+// the 154 that the matrix cores give a library's product.)
 #include <math.h>
 
 #include "attention_forward.hpp"
@@ -238,6 +240,10 @@ hipError_t by_size(const AttentionParams &p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream) {
+  // tiles of 16 rows for sequences of few (8 heads, the mean of their rows: in float32
+  // of 64 elements 10 42 us for 83, 40 26 for 35; in bfloat16 of 128 10 54 for 80, 40 23
+  // for 27, 64 44 for 36 with two waves a SIMD)
+  if (p.tokens / p.batch <= 40) return launch_attention_short(p, dtype, stream);
   return dtype == kF32 ? by_size<F32, 32>(p, stream) : by_size<BF16, 64>(p, stream);
 }
 

@@ -9,8 +9,8 @@
 // SIMD cover each other.  (2048 sequences of up to 20 rows, 4 heads of 64 in float32:
 // 24 us, 3.5 TB/s of what must be read and written, where tiles of 32 took 45; the
 // gradient 83 us for 120.  One kernel for all of the gradient, which reads the rows of
-// short sequences once, took 80: it leaves registers for fewer waves, and of 128
-// elements 410 us for 385, 211 for 169 in bfloat16.)
+// short sequences once, leaves registers for fewer waves: of 8 heads it took 128 us
+// for 134, but of 128 elements in bfloat16 211 for 169.)
 #include <math.h>
 
 #include "attention_forward.hpp"

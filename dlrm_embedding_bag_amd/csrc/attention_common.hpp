@@ -484,6 +484,92 @@ __device__ __forceinline__ Item item_of(int64_t i, int64_t tiles, int heads) {
   return {(uint32_t)(tiles - 1 - t), (int)r};
 }
 
+// Calls of few sequences and not many workgroups: their tiles go out by the keys that
+// they see, most first, and where a CU holds PAIRS every second 256 of them in reverse,
+// so that one of its two is long where the other is short.  (Seven pieces after 777
+// keys, 468 workgroups: 45 us for 50; three sequences of up to 2500, 12 heads of 128, in
+// float32 637 for 794; one of 1466 keys in 80 pays 2.5 us for the search.)
+__device__ __forceinline__ bool in_order_of_work(int64_t items, int64_t batch, int64_t kv_tokens) {
+  return items > 256 && items <= 1024 && batch <= 16 && kv_tokens < 1 << 30;
+}
+template <bool PAIRS>
+__device__ __forceinline__ int64_t pair_up(int64_t item, int64_t items) {
+  const int i = (int)item, n = (int)items, at = i & 255, block = i - at;
+  return PAIRS && block & 256 ? block + (n - block < 256 ? n - block : 256) - 1 - at : i;
+}
+// The tile of ROWS rows that is number `rank` in that order; behind them come those
+// outside all sequences.  The least number of keys that it may see is found by
+// counting, for a number in each lane.
+template <int ROWS>
+__device__ __forceinline__ Tile tile_of_rank(const int32_t *offsets, const int32_t *kv_offsets,
+                                             uint32_t batch, int total, int kv_total, int causal,
+                                             int rank) {
+  const uint32_t lane = threadIdx.x % kWave;
+  int first = 0, rows = 0, keys = 0;   // of the lane's sequence
+  if (lane < batch) {
+    first = segment_start(offsets, batch, total, lane + 1);
+    const int last = segment_start(offsets, batch, total, lane + 2);
+    rows = last > first ? last - first : 0;
+    keys = rows;
+    if (kv_offsets) {
+      keys = segment_start(kv_offsets, batch, kv_total, lane + 2) -
+             segment_start(kv_offsets, batch, kv_total, lane + 1);
+      keys = keys > 0 ? keys : 0;
+    }
+  }
+  // tiles of a sequence that see `least` keys or more: its last ones
+  auto seeing = [&](int rows, int keys, int least) __attribute__((always_inline)) {
+    const int end = causal && least > 0 ? rows - keys + least : 0;   // rows to a tile's end
+    const int none = end > 0 ? (end - 1) / ROWS : 0;
+    return least > keys ? 0 : (rows + ROWS - 1) / ROWS - none;
+  };
+  auto count = [&](int least) __attribute__((always_inline)) {
+    int n = 0;
+    for (uint32_t b = 0; b < batch; ++b)
+      n += seeing(__builtin_amdgcn_readlane(rows, b), __builtin_amdgcn_readlane(keys, b), least);
+    return n;
+  };
+  Tile t;
+  const int all = uniform(count(0));
+  if (rank >= all) {
+    rank -= all;
+    const int before = uniform(segment_start(offsets, batch, total, 1));
+    const int behind = uniform(segment_start(offsets, batch, total, batch + 1));
+    const int n = (before + ROWS - 1) / ROWS;
+    t.sequence = -1;
+    t.first = rank < n ? 0 : behind;
+    const int64_t row = t.first + (int64_t)(rank < n ? rank : rank - n) * ROWS;
+    const int last = rank < n ? before : total;
+    t.row = row < last ? (int)row : last;
+    t.left = last - t.row;
+    return t;
+  }
+  int most = 0, span = 1 << 30;   // it sees most .. most + span - 1
+  while (span > 1) {
+    const int step = __any(keys - most >= span / 64) ? span / 64 : span / 4096;
+    const int each = step > 0 ? step : 1;
+    const uint64_t mask = __ballot(count(most + (int)lane * each) > rank);
+    most += (63 - __builtin_clzll(mask | 1)) * each;
+    span = each;
+  }
+  rank -= uniform(count(most + 1));
+  const int at_most = seeing(rows, keys, most), mine = at_most - seeing(rows, keys, most + 1);
+  int upto = mine;
+#pragma unroll
+  for (int x = 1; x < 16; x *= 2) {
+    const int other = __shfl_up(upto, x);
+    upto += (int)lane >= x ? other : 0;
+  }
+  const uint64_t mask = __ballot(lane < batch && upto > rank);
+  const int b = mask ? __builtin_ctzll(mask) : 0;
+  const int n = (rows + ROWS - 1) / ROWS, tile = n - at_most + rank - (upto - mine);
+  t.sequence = b;
+  t.first = __builtin_amdgcn_readlane(first, b);
+  t.row = t.first + __builtin_amdgcn_readlane(tile, b) * ROWS;
+  t.left = t.first + __builtin_amdgcn_readlane(rows, b) - t.row;
+  return t;
+}
+
 // A scalar whose uses stay within the loop over items: what follows from it would
 // else be made before the loop and kept, beyond the registers that there are.
 __device__ __forceinline__ int in_loop(int v) {

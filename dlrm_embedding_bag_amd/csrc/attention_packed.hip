@@ -49,9 +49,14 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, 2) void attention_kernel(Atte
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int dim = in_loop(p.dim);
-    const Item at = item_of(item, tile_count(p.tokens, p.batch, BM), p.heads);
+    const int64_t tiles = tile_count(p.tokens, p.batch, BM);
+    constexpr bool PAIRS = 4 * GROUPS * L::SIZE * 16 <= 80 << 10;   // as its LDS allows
+    const bool by_work = WAVES > 1 && in_order_of_work(items, p.batch, p.kv_tokens);
+    const Item at = item_of(by_work ? pair_up<PAIRS>(item, items) : item, tiles, p.heads);
     const int head = at.head;
-    const Tile t = find_tile(p.offsets, p.batch, p.tokens, at.tile, BM);
+    const Tile t = by_work ? tile_of_rank<BM>(p.offsets, p.kv_offsets, p.batch, p.tokens,
+                                              p.kv_tokens, p.causal, (int)(tiles - 1 - at.tile))
+                           : find_tile(p.offsets, p.batch, p.tokens, at.tile, BM);
     if (t.left <= 0) continue;
     const int mine = wave * 32 + (lane & 31);   // row of the tile
     if (t.sequence < 0) {

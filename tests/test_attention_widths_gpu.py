@@ -54,6 +54,50 @@ def test_many_rows_of_many_heads(kind, tokens, dim):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,past", [([300, 0, 77, 129, 1, 200], None),
+                                          ([200, 64, 0, 300], [-150, 500, 9, -300]),
+                                          ([40] * 17, None)])
+def test_rows_outside_sequences_of_many_heads(lengths, past, causal, kind):
+    """Rows before the first sequence and behind the last, with tiles enough that
+    workgroups go out by their work: each row is written once, as it should be."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    lead, tail, heads, kv = 150, 200, 40, 20
+    off, koff, q, k, v, grad = _packed_inputs(lengths, past, heads, kv, 64, kind)
+    n = int(off[-1])
+    wide = [torch.cat([torch.full((a, *t.shape[1:]), float("nan"), dtype=t.dtype), t,
+                       torch.full((b, *t.shape[1:]), float("nan"), dtype=t.dtype)]).cuda()
+            for t, a, b in ((q, lead, tail), (grad, lead, tail))]
+    if past is None:
+        wk, wv = (torch.cat([torch.full((lead, kv, 64), float("nan"), dtype=t.dtype), t,
+                             torch.full((tail, kv, 64), float("nan"), dtype=t.dtype)]).cuda()
+                  for t in (k, v))
+    else:
+        wk, wv = k.cuda(), v.cuda()
+    offs = ((off + lead).cuda(), None if koff is None else koff.cuda())
+    out, lse = fw.attention_packed(wide[0], wk, wv, *offs, causal=causal)
+    pick = [0, 19]
+    rows = [0, 1, 38, 39]
+    inside = slice(lead, lead + n)
+    want = _attention_want(q[:, rows], k[:, pick], v[:, pick], off, koff, causal, 0.125, kind)
+    _assert_within(_np64(out[inside, rows]), want[0], want[1], "out")
+    _assert_within(_np64(lse[inside, rows]), want[2], want[3], "lse")
+    got = fw.attention_packed_grad(wide[1], wide[0], wk, wv, out, lse, *offs, causal=causal)
+    want, tol = _gradient_want(grad[:, rows], q[:, rows], k[:, pick], v[:, pick], out[inside, rows],
+                               lse[inside, rows], off, koff, causal, 0.125, kind)
+    keys = inside if past is None else slice(None)
+    for a, w, t, what, at in zip((got[0][inside], got[1][keys], got[2][keys]), want, tol, "qkv",
+                                 (rows, pick, pick)):
+        _assert_within(_np64(a[:, at]), w, t, what)
+    for part in (slice(0, lead), slice(lead + n, None)):
+        assert not out[part].any() and (lse[part] == float("-inf")).all() and not got[0][part].any()
+        if past is None:
+            assert not got[1][part].any() and not got[2][part].any()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", ["slice", "heads"])
 @pytest.mark.parametrize("lengths", [[3, 16, 7, 0, 18], [60, 70], [257, 60]])
 def test_layouts(lengths, layout, kind):

@@ -135,17 +135,17 @@ __device__ __forceinline__ double row_sum(double v, int lanes) {
 }
 
 __device__ __forceinline__ void make_turns(const RopeParams &p, int64_t token0, int tokens,
-                                           float2 (*turns)[kMaxPairs]) {
+                                           float2 *turns) {
   for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
     const int t = i / p.pairs, j = i - t * p.pairs;
-    turns[t][j] = turn_of(p.positions[token0 + t], p.freqs[j]);
+    turns[i] = turn_of(p.positions[token0 + t], p.freqs[j]);
   }
 }
 
 template <typename T, int N, bool INTER>
 __device__ __forceinline__ void forward_rows(const RopeParams &p, const RopeSide &side,
                                              int64_t token0, int tokens, int lanes,
-                                             const Slot<N> &s, float2 (*turns)[kMaxPairs]) {
+                                             const Slot<N> &s, const float2 *turns) {
   using S = typename T::S;
   if (side.heads == 0) return;
   float w[2 * N];
@@ -168,19 +168,19 @@ __device__ __forceinline__ void forward_rows(const RopeParams &p, const RopeSide
     if (on) {
 #pragma unroll
       for (int e = 0; e < 2 * N; ++e) v[e] = v[e] * u * w[e];
-      if (s.turned) turn<N, INTER, false>(turns[t] + s.pair, v);
+      if (s.turned) turn<N, INTER, false>(turns + t * p.pairs + s.pair, v);
       store_slot<T, N>((S *)side.y + (token0 + t) * side.y_token + h * side.y_head, s, v);
     }
   }
 }
 
 template <typename T, int N, bool INTER, int TOKENS>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p, int lanes) {
-  __shared__ float2 turns[TOKENS][kMaxPairs];
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p, int lanes, int each) {
+  __shared__ float2 turns[TOKENS * kMaxPairs];
   const Slot<N> s = slot_of<N, INTER>(threadIdx.x & (lanes - 1), p.dim, p.pairs);
-  for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < p.tokens;
-       t0 += (int64_t)gridDim.x * TOKENS) {
-    const int tokens = (int)(p.tokens - t0 < TOKENS ? p.tokens - t0 : TOKENS);
+  for (int64_t t0 = (int64_t)blockIdx.x * each; t0 < p.tokens;
+       t0 += (int64_t)gridDim.x * each) {
+    const int tokens = (int)(p.tokens - t0 < each ? p.tokens - t0 : each);
     make_turns(p, t0, tokens, turns);
     __syncthreads();
     forward_rows<T, N, INTER>(p, p.q, t0, tokens, lanes, s, turns);
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p, int lanes)
 template <typename T, int N, bool INTER>
 __device__ __forceinline__ void backward_rows(const RopeParams &p, const RopeSide &side,
                                               int64_t token0, int tokens, int lanes,
-                                              const Slot<N> &s, float2 (*turns)[kMaxPairs],
+                                              const Slot<N> &s, const float2 *turns,
                                               const float (&w)[2 * N], float (&dw)[2 * N]) {
   using S = typename T::S;
   if (side.heads == 0) return;
@@ -206,7 +206,7 @@ __device__ __forceinline__ void backward_rows(const RopeParams &p, const RopeSid
     if (on) {
       load_slot<T, N>((const S *)side.x + (token0 + t) * side.x_token + h * side.x_head, s, v);
       load_slot<T, N>((const S *)side.grad + (token0 + t) * side.g_token + h * side.g_head, s, d);
-      if (s.turned) turn<N, INTER, true>(turns[t] + s.pair, d);
+      if (s.turned) turn<N, INTER, true>(turns + t * p.pairs + s.pair, d);
     }
     double sum = 0.0, dot = 0.0;
 #pragma unroll
@@ -257,8 +257,8 @@ __device__ __forceinline__ void put_weight_sums(const float (&dw)[2 * N], const 
 
 template <typename T, int N, bool INTER, int TOKENS>
 __global__ __launch_bounds__(kThreads) void rope_grad_kernel(RopeParams p, int lanes,
-                                                             float *partial) {
-  __shared__ float2 turns[TOKENS][kMaxPairs];
+                                                             int each, float *partial) {
+  __shared__ float2 turns[TOKENS * kMaxPairs];
   __shared__ float sums[8 * kMaxRopeDim];
   const Slot<N> s = slot_of<N, INTER>(threadIdx.x & (lanes - 1), p.dim, p.pairs);
   float wq[2 * N], wk[2 * N], dq[2 * N], dk[2 * N];
@@ -269,9 +269,9 @@ __global__ __launch_bounds__(kThreads) void rope_grad_kernel(RopeParams p, int l
     wk[e] = s.there && p.k.weight ? p.k.weight[at] : 1.0f;
     dq[e] = dk[e] = 0.0f;
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < p.tokens;
-       t0 += (int64_t)gridDim.x * TOKENS) {
-    const int tokens = (int)(p.tokens - t0 < TOKENS ? p.tokens - t0 : TOKENS);
+  for (int64_t t0 = (int64_t)blockIdx.x * each; t0 < p.tokens;
+       t0 += (int64_t)gridDim.x * each) {
+    const int tokens = (int)(p.tokens - t0 < each ? p.tokens - t0 : each);
     make_turns(p, t0, tokens, turns);
     __syncthreads();
     backward_rows<T, N, INTER>(p, p.q, t0, tokens, lanes, s, turns, wq, dq);
@@ -315,11 +315,21 @@ constexpr int kBlockTokens = 4;
 // take a workgroup each.
 bool many(int64_t tokens) { return tokens >= 1024; }
 
-int64_t token_blocks(int64_t tokens) {
-  return many(tokens) ? (tokens + kBlockTokens - 1) / kBlockTokens : tokens;
+// Four tokens or more, where few and short rows would leave lanes without one (28785
+// tokens of 4 + 2 heads of 8 in bfloat16: 12 us for 18, gradient 24 for 51; 100000 of
+// 1 + 1 of 64 34 for 105 and 63 for 182), as many as LDS holds
+// the turns of, and workgroups are left for all CUs.
+int tokens_each(const RopeParams &p, int lanes) {
+  if (!many(p.tokens)) return 1;
+  const int heads = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;
+  int each = kBlockTokens;
+  while ((int64_t)each * heads * lanes < kThreads && each * 2 * p.pairs <= kBlockTokens * kMaxPairs &&
+         p.tokens / (each * 2) >= kGradBlocks)
+    each *= 2;
+  return each;
 }
-int grad_blocks(int64_t tokens) {
-  const int64_t b = token_blocks(tokens);
+int grad_blocks(int64_t tokens, int each) {
+  const int64_t b = (tokens + each - 1) / each;
   return (int)(b < kGradBlocks ? b : kGradBlocks);
 }
 
@@ -335,25 +345,26 @@ void each_kind(const RopeParams &p, F &&f) {
 
 template <typename T, int N, bool INTER>
 hipError_t run_forward(const RopeParams &p, int lanes, hipStream_t stream) {
-  const int64_t blocks = token_blocks(p.tokens);
+  const int each = tokens_each(p, lanes);
+  const int64_t blocks = (p.tokens + each - 1) / each;
   const uint32_t grid = (uint32_t)(blocks < (1 << 22) ? blocks : 1 << 22);
   if (many(p.tokens))
     launch_kernel(rope_kernel<T, N, INTER, kBlockTokens>, dim3(grid), dim3(kThreads), 0, stream, p,
-                  lanes);
+                  lanes, each);
   else
-    launch_kernel(rope_kernel<T, N, INTER, 1>, dim3(grid), dim3(kThreads), 0, stream, p, lanes);
+    launch_kernel(rope_kernel<T, N, INTER, 1>, dim3(grid), dim3(kThreads), 0, stream, p, lanes, each);
   return hipGetLastError();
 }
 
 template <typename T, int N, bool INTER>
 hipError_t run_backward(const RopeParams &p, int lanes, float *partial, hipStream_t stream) {
-  const int blocks = grad_blocks(p.tokens);
+  const int each = tokens_each(p, lanes), blocks = grad_blocks(p.tokens, each);
   if (many(p.tokens))
     launch_kernel(rope_grad_kernel<T, N, INTER, kBlockTokens>, dim3(blocks), dim3(kThreads), 0,
-                  stream, p, lanes, partial);
+                  stream, p, lanes, each, partial);
   else if (p.tokens)
     launch_kernel(rope_grad_kernel<T, N, INTER, 1>, dim3(blocks), dim3(kThreads), 0, stream, p,
-                  lanes, partial);
+                  lanes, each, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.q.dweight && !p.k.dweight)) return e;
   launch_kernel(rope_weight_kernel, dim3((p.dim + 15) / 16, 2), dim3(kSumThreads), 0,
@@ -364,7 +375,7 @@ hipError_t run_backward(const RopeParams &p, int lanes, float *partial, hipStrea
 }  // namespace
 
 size_t rope_grad_workspace(int64_t tokens, int dim) {
-  return (size_t)grad_blocks(tokens) * 2 * dim * sizeof(float);
+  return (size_t)grad_blocks(tokens, many(tokens) ? kBlockTokens : 1) * 2 * dim * sizeof(float);
 }
 
 hipError_t launch_rope(const RopeParams &p, int dtype, bool interleaved, hipStream_t stream) {

@@ -1,9 +1,10 @@
 """GPU tests of packed attention and its gradient in every width that sequences call
 for: many of few rows, some of about a hundred, few long ones of few heads, and enough
-rows and heads for the widest workgroups.  References and the counting of roundings
+rows and heads for the widest workgroups; and of the rotation of few heads.  References and the counting of roundings
 are those of test_attention_ops_gpu.py."""
 import pytest
 
+import test_attention_ops_gpu as ops
 from conftest import gpu_available
 from test_attention_ops_gpu import (_assert_within, _attention_want, _dt, _gen, _gradient_want,
                                     _laid, _np64, _packed_inputs, _randn)
@@ -138,6 +139,15 @@ def test_masked_values_that_are_not_finite(length, at, heads, bad, kind):
     out[at:length, 1, 3] = want[at:length, 1, 3]
     # (the careful way adds the same products in the same order, but for these)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n,heads,kv,dim,pairs", [(4100, 1, 1, 64, 32), (8207, 2, 0, 8, 4),
+                                                  (33000, 1, 2, 8, 4), (5000, 3, 1, 128, 64)])
+def test_rotation_of_many_tokens_of_few_heads(n, heads, kv, dim, pairs, kind):
+    """(several tokens a workgroup, the last of them not whole)"""
+    ops.test_rope(n, heads, kv, dim, pairs, False, kind)
+    ops.test_rope_gradient(n, heads, kv, dim, pairs, True, kind)
 
 
 def test_offsets_that_decrease_stay_within_the_tensors():

@@ -317,8 +317,8 @@ bool many(int64_t tokens) { return tokens >= 1024; }
 
 // Four tokens or more, where few and short rows would leave lanes without one (28785
 // tokens of 4 + 2 heads of 8 in bfloat16: 12 us for 18, gradient 24 for 51; 100000 of
-// 1 + 1 of 64 34 for 105 and 63 for 182), as many as LDS holds
-// the turns of, and workgroups are left for all CUs.
+// 1 + 1 of 64 34 for 105 and 63 for 182): as many as LDS holds the turns of, and
+// workgroups are left for all CUs.
 int tokens_each(const RopeParams &p, int lanes) {
   if (!many(p.tokens)) return 1;
   const int heads = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;

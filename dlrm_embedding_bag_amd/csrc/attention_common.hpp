@@ -601,6 +601,15 @@ inline bool few_tiles(int64_t tokens, int heads) {
   return tokens / 128 * heads < (sizeof(typename T::S) == 4 ? 512 : 256);
 }
 
+// Few rows that see many keys, in fewer heads than there are CUs for two of: no lone
+// wave walks all the keys then.  (32 sequences of 20 rows after 1000 keys, 8 heads of
+// 64: 51 us for 105 in float32, 19 for 39 in bfloat16; of 4 of 8 rows after 4000, 8
+// heads of 128 the gradient 449 for 672 and 93 for 274.  256 sequences fill the card
+// with waves: 302 for 692 the other way round.)
+inline bool few_of_long(int64_t batch, int heads, int64_t kv_tokens) {
+  return kv_tokens / batch > 256 && batch * heads <= 512;
+}
+
 // Workgroups for that many items; each takes those a grid apart.
 inline uint32_t grid_of(int64_t items) {
   return (uint32_t)(items < (1 << 22) ? items : 1 << 22);

@@ -494,7 +494,8 @@ hipError_t launch_attention_grad(const AttentionGradParams &p, int dtype, void *
   // of 64 elements 10 135 us for 214, 40 84 for 101; of 128 10 385 for 535, 40 203 for
   // 210; in bfloat16 of 128 10 169 for 244, 24 94 for 110, but 94 for 78 where all heads
   // share a key head's)
-  if (p.tokens / p.batch <= (dtype == kF32 ? 40 : 16))
+  if (p.tokens / p.batch <= (dtype == kF32 ? 40 : 16) &&
+      !few_of_long(p.batch, p.heads, p.kv_tokens))
     return launch_attention_grad_short(p, dtype, workspace, stream);
   float *ws = (float *)workspace;
   return dtype == kF32 ? by_dim<F32>(p, ws, stream) : by_dim<BF16>(p, ws, stream);

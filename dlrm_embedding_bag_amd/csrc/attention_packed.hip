@@ -237,7 +237,8 @@ hipError_t by_dim(const AttentionParams &p, hipStream_t stream) {
 // 8 heads of 64: 12 us for 17 in bfloat16, 23 for 38 in float32); else four waves.
 template <typename T, int BN>
 hipError_t by_size(const AttentionParams &p, hipStream_t stream) {
-  if (p.tokens / p.batch <= 128) return by_dim<T, 1, 32, 1>(p, stream);
+  if (p.tokens / p.batch <= 128 && !few_of_long(p.batch, p.heads, p.kv_tokens))
+    return by_dim<T, 1, 32, 1>(p, stream);
   if (few_tiles<T>(p.tokens, p.heads)) return by_dim<T, 2, BN, 2>(p, stream);
   return by_dim<T, 4, BN, 1>(p, stream);
 }
@@ -248,7 +249,8 @@ hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t str
   // tiles of 16 rows for sequences of few (8 heads, the mean of their rows: in float32
   // of 64 elements 10 42 us for 83, 40 26 for 35; in bfloat16 of 128 10 54 for 80, 40 23
   // for 27, 64 44 for 36 with two waves a SIMD)
-  if (p.tokens / p.batch <= 40) return launch_attention_short(p, dtype, stream);
+  if (p.tokens / p.batch <= 40 && !few_of_long(p.batch, p.heads, p.kv_tokens))
+    return launch_attention_short(p, dtype, stream);
   return dtype == kF32 ? by_size<F32, 32>(p, stream) : by_size<BF16, 64>(p, stream);
 }
 

@@ -17,6 +17,8 @@ SHORT = [([0, 1, 15, 16, 17, 33, 2, 0, 5, 14], None, 3, 1),
          ([16] * 5 + [1] * 7, [0, 3, 16, -9, 40, 0, 1, 31, 0, 0, -1, 100], 2, 2),
          ([1] * 40, [0, 5, 15, 16] * 10, 8, 2), ([32, 0, 0, 0], [0, 7, 0, 20], 5, 5)]
 SOME = [([40, 60, 90, 33], None, 3, 1), ([100, 50], [-60, 70], 2, 2)]
+LONG = [([1, 8, 0, 20], [700, 300, 400, 1200], 4, 2), ([3, 60], [600, 290], 3, 1),
+        ([5] * 300, [270] * 300, 2, 1)]
 FEW = [([129, 300], None, 3, 1), ([260, 131], [-140, 63], 2, 2), ([513], [64], 1, 1)]
 
 
@@ -41,9 +43,9 @@ def _check(lengths, past, heads, kv, dim, causal, kind, pick=None):
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("lengths,past,heads,kv", SHORT + SOME + FEW)
+@pytest.mark.parametrize("lengths,past,heads,kv", SHORT + SOME + LONG + FEW)
 def test_widths(lengths, past, heads, kv, causal, kind):
-    for dim in (8, 32, 40, 64, 88, 96, 104, 128):
+    for dim in (8, 32, 40, 64, 88, 96, 104, 128) if len(lengths) < 100 else (64,):
         _check(lengths, past, heads, kv, dim, causal, kind)
 
 

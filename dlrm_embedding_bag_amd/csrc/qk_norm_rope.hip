@@ -134,6 +134,25 @@ __device__ __forceinline__ double row_sum(double v, int lanes) {
   return v;
 }
 
+// v *= 1 / rms, in float32 where that is a normal number.  Rows of 3e-39 or of 1e38 with
+// an eps that is no larger have a reciprocal beyond, and so has any row of zeros with an
+// eps below 1e-77, though the products are numbers: those are made in 64 bits.
+template <int N>
+__device__ __forceinline__ void times_inverse(float (&v)[2 * N], double inv) {
+  const float u = (float)inv;
+  if (__builtin_isnormal(u)) {
+#pragma unroll
+    for (int e = 0; e < 2 * N; ++e) v[e] *= u;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2 * N; ++e) {
+      float x = v[e];
+      asm volatile("" : "+v"(x));   // (else the sum's 64-bit elements are kept for here)
+      v[e] = (float)((double)x * inv);
+    }
+  }
+}
+
 __device__ __forceinline__ void make_turns(const RopeParams &p, int64_t token0, int tokens,
                                            float2 *turns) {
   for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
@@ -164,10 +183,11 @@ __device__ __forceinline__ void forward_rows(const RopeParams &p, const RopeSide
     double sum = 0.0;
 #pragma unroll
     for (int e = 0; e < 2 * N; ++e) sum = __builtin_fma((double)v[e], (double)v[e], sum);
-    const float u = (float)(1.0 / sqrt(row_sum(sum, lanes) / p.dim + p.eps));
+    const double inv = 1.0 / sqrt(row_sum(sum, lanes) / p.dim + p.eps);
     if (on) {
+      times_inverse<N>(v, inv);
 #pragma unroll
-      for (int e = 0; e < 2 * N; ++e) v[e] = v[e] * u * w[e];
+      for (int e = 0; e < 2 * N; ++e) v[e] *= w[e];
       if (s.turned) turn<N, INTER, false>(turns + t * p.pairs + s.pair, v);
       store_slot<T, N>((S *)side.y + (token0 + t) * side.y_token + h * side.y_head, s, v);
     }
@@ -215,15 +235,15 @@ __device__ __forceinline__ void backward_rows(const RopeParams &p, const RopeSid
       dot = __builtin_fma((double)(d[e] * w[e]), (double)v[e], dot);
     }
     const double inv = 1.0 / sqrt(row_sum(sum, lanes) / p.dim + p.eps);
-    const float u = (float)inv;
     const float along = (float)(row_sum(dot, lanes) * inv / p.dim);   // mean(g u)
     if (on) {
+      times_inverse<N>(v, inv);
 #pragma unroll
       for (int e = 0; e < 2 * N; ++e) {
-        const float n = v[e] * u;
-        dw[e] = __builtin_fmaf(d[e], n, dw[e]);
-        v[e] = u * __builtin_fmaf(-n, along, d[e] * w[e]);
+        dw[e] = __builtin_fmaf(d[e], v[e], dw[e]);
+        v[e] = __builtin_fmaf(-v[e], along, d[e] * w[e]);
       }
+      times_inverse<N>(v, inv);
       store_slot<T, N>((S *)side.y + (token0 + t) * side.y_token + h * side.y_head, s, v);
     }
   }

@@ -46,6 +46,9 @@ bool aligned_rows(const void *p, int64_t n, int64_t token, int32_t heads, int64_
   const int64_t e = 16 / size_of(dtype);
   return aligned16(p) && (n <= 1 || token % e == 0) && (heads <= 1 || head % e == 0);
 }
+// The kernels keep scores in units of log 2, so that factor has to be a number too.
+bool scale_of_scores(float scale) { return scale > 0.0f && scale * kLog2e < INFINITY; }
+
 // Tiles of up to 128 rows are addressed within 2 GiB.
 constexpr int64_t kMaxTokenStride = (1 << 22) - 1024;
 bool near_rows(int64_t n, std::initializer_list<int64_t> strides) {
@@ -59,7 +62,7 @@ int attention_shape(int64_t tokens, int64_t kv_tokens, int64_t batch, int32_t he
   if (tokens < 0 || tokens > INT32_MAX || kv_tokens < 0 || kv_tokens > INT32_MAX || batch < 1 ||
       batch >= INT32_MAX || heads < 1 || heads > kMaxHeads || kv_heads < 1 || kv_heads > heads ||
       heads % kv_heads || dim < 8 || dim % 8 || !float_dtype(dtype) ||
-      (causal != 0 && causal != 1) || !(scale > 0.0f) || !(scale < INFINITY))
+      (causal != 0 && causal != 1) || !scale_of_scores(scale))
     return DLRM_ERR_SHAPE;
   return dim > DLRM_MAX_ATTENTION_DIM ? DLRM_ERR_UNSUPPORTED : DLRM_OK;
 }
@@ -349,7 +352,7 @@ int attention_cached(int64_t batch, int32_t heads, int32_t kv_heads, int32_t dim
                      void *stream) {
   if (batch < 0 || batch > INT32_MAX || heads < 1 || heads > kMaxHeads || kv_heads < 1 ||
       kv_heads > heads || heads % kv_heads || !float_dtype(dtype) || max_pages < 0 ||
-      max_pages > INT32_MAX || ld_table < 0 || !(scale > 0.0f) || !(scale < INFINITY))
+      max_pages > INT32_MAX || ld_table < 0 || !scale_of_scores(scale))
     return DLRM_ERR_SHAPE;
   const int bad = cache_shape(kv_heads, dim, pages, page, bits);
   if (bad) return bad;

@@ -302,6 +302,7 @@ hipError_t launch_rope_grad(const RopeParams &p, int dtype, bool interleaved, vo
                             hipStream_t stream);
 
 // Attention over packed sequences (attention_packed.hip, attention_grad.hip).
+constexpr float kLog2e = 1.4426950408889634f;
 struct HeadRows {  // (tokens, heads, dim), strides in elements
   const void *data;
   int64_t token, head;

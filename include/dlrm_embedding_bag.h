@@ -762,7 +762,9 @@ DLRM_API int qk_norm_rope_grad(
  *               kv_tokens is tokens).  Offsets that are out of order give
  *               undefined results within the tensors
  *   causal      0 or 1
- *   scale       finite, > 0
+ *   scale       > 0 and at most 2.35e38: scores are kept in units of log 2, and
+ *               scale * log2(e) has to be a float32 number.  For the same reason a
+ *               score beyond 2.35e38 either way counts as infinite
  *   fill        what becomes of rows outside all sequences: 0 they are left as
  *               they are; + 1 they are zero in out; + 2 they are -inf in lse
  *   lse         (tokens, heads) float32, or NULL
@@ -869,7 +871,7 @@ DLRM_API int kv_cache_read(int64_t tokens, int32_t heads, int32_t dim, int32_t d
  *   table    (batch, max_pages) int32, row stride ld_table (0: one row for all)
  *   lengths  (batch,) int32, at most max_pages * page (what lies beyond is not
  *            there)
- *   scale    finite, > 0
+ *   scale    as in attention_packed
  *   workspace  16-byte aligned, at least attention_cached_workspace_bytes bytes
  *              (which may return 0, and does for sizes that the call refuses); it
  *              needs no clearing.  Its size and the split of the work depend on

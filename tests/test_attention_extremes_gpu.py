@@ -64,3 +64,24 @@ def test_rope_of_rows_and_eps_far_from_one(eps, sizes, dim, pairs, inter, kind):
         terms = (np.abs(unit) * size).sum((0, 1))
         _assert_within(_np64(back[2 + i]), (dv * unit).sum((0, 1)),
                        (20 + unit.shape[0] * unit.shape[1]) * U32 * terms + TINY, what + " weight")
+
+
+# ----------------------------------------------------------- packed attention --
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_attention_with_a_scale_next_to_the_limit(kind):
+    """Scores of up to 128 of products of 2^-120, all of them powers of two or so."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    q, k = torch.zeros(30, 1, 8), torch.zeros(30, 1, 8)
+    g = _gen(1)
+    q[:, 0, 3] = 2.0 ** -60 * (0.5 + torch.rand(30, generator=g) / 2)
+    k[:, 0, 3] = 2.0 ** -60 * (0.5 + torch.rand(30, generator=g) / 2)
+    q, k, v = (t.to(_dt(kind)) for t in (q, k, _randn(g, 30, 1, 8)))
+    off = torch.tensor([0, 30], dtype=torch.int32)
+    want = _attention_want(q, k, v, off, None, True, 2.0 ** 127, kind)
+    out, lse = fw.attention_packed(q.cuda(), k.cuda(), v.cuda(), off.cuda(), scale=2.0 ** 127)
+    _assert_within(_np64(out), want[0], want[1], "out")
+    _assert_within(_np64(lse), want[2], want[3], "lse")
+    with pytest.raises(fw.DlrmError, match="attention"):
+        fw.attention_packed(q.cuda(), k.cuda(), v.cuda(), off.cuda(), scale=2.4e38)

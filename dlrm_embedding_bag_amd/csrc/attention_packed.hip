@@ -153,9 +153,10 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, 2) void attention_kernel(Atte
     };
     // A value that is not finite must not reach the rows that do not see it, and
     // zero times it is not zero: from the first tile on that some row does not see
-    // whole, such values are left out, and added after the last tile.
+    // whole, such values are left out, and added after the last tile.  (Rows of values
+    // that repeat or overlap stand behind the last key too, where others are zeros.)
     auto round_of = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
-      if (p.causal && seen.tile_all - n * GROUPS * BN < GROUPS * BN &&
+      if ((p.causal || p.v.token < dim) && seen.tile_all - n * GROUPS * BN < GROUPS * BN &&
           clean<T, L::SIZE, WAVES, GROUPS>(v, found, wave, part, lane))
         loose = loose < 0 ? n : loose;
       work(k, v, n);

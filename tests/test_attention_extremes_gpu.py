@@ -85,3 +85,38 @@ def test_attention_with_a_scale_next_to_the_limit(kind):
     _assert_within(_np64(lse), want[2], want[3], "lse")
     with pytest.raises(fw.DlrmError, match="attention"):
         fw.attention_packed(q.cuda(), k.cuda(), v.cuda(), off.cuda(), scale=2.4e38)
+
+
+# Lengths and heads that go to lone waves of 16 and of 32 rows, to two groups of waves
+# and to four waves; none fills its last tile of keys.
+KINDS = [([20, 7], 2), ([100, 90], 2), ([301], 2), ([4100], 16)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lengths,heads", KINDS)
+def test_attention_of_repeated_values_that_are_not_finite(lengths, heads, causal, kind):
+    """One row of values for all keys (stride 0), and rows that overlap, as the same
+    rows one after another: behind the last key there is none of them."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, _, _ = (None if t is None else t.cuda()
+                          for t in _packed_inputs(lengths, None, heads, heads, 32, kind))
+    n = len(q)
+    row = _randn(_gen(2), 1, heads, 32).to(_dt(kind)).cuda()
+    row[0, 0, 5], row[0, 1, 6], row[0, 1, 7] = math.inf, -math.inf, math.nan
+    same = row.expand(n, -1, -1)
+    out, lse = fw.attention_packed(q, k, same, off, causal=causal)
+    want, wlse = fw.attention_packed(q, k, same.contiguous(), off, causal=causal)
+    assert torch.equal(lse, wlse) and torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+    assert (out[:, 0, 5] == math.inf).all() and (out[:, 1, 6] == -math.inf).all()
+    assert torch.equal(out.isnan(), same.isnan())
+
+    flat = _randn(_gen(3), 8 * n + 24).to(_dt(kind)).cuda()
+    flat[-1], flat[-30] = math.inf, -math.inf          # of the last row, of the last four
+    over = flat.as_strided((n, 1, 32), (8, 32, 1)).expand(-1, heads, -1)
+    out, lse = fw.attention_packed(q, k, over, off, causal=causal)
+    want, wlse = fw.attention_packed(q, k, over.contiguous(), off, causal=causal)
+    assert torch.equal(lse, wlse) and torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+    assert not out.isnan().any() and out.isinf().any()

@@ -26,16 +26,21 @@ __device__ __forceinline__ uint32_t finite(uint32_t w) {   // zeros in their pla
 }
 
 // A tile of values in LDS for each group of WAVES waves: whether one holds a value
-// that is not finite, for all waves; if so it is zero there when this returns.
+// that is not finite, for all waves; if so it is zero there when this returns.  A group
+// whose tile is not `there` has nothing to say: what its part of LDS holds was left by
+// whoever had it before.
 template <typename T, int SIZE, int WAVES, int GROUPS>
-__device__ __forceinline__ bool clean(LdsChunks v, int *found, int wave, int part, int lane) {
+__device__ __forceinline__ bool clean(LdsChunks v, bool there, int *found, int wave, int part,
+                                      int lane) {
   constexpr int EACH = SIZE / (WAVES * kWave);
   uint32_t others = 0;
+  if (GROUPS == 1 || there) {
 #pragma unroll
-  for (int i = 0; i < EACH; ++i) {
-    const u32x4_t w = v[(i * WAVES + wave) * kWave + lane];
+    for (int i = 0; i < EACH; ++i) {
+      const u32x4_t w = v[(i * WAVES + wave) * kWave + lane];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) others |= not_finite<T>(w[e]);
+      for (int e = 0; e < 4; ++e) others |= not_finite<T>(w[e]);
+    }
   }
   const bool mine = __any(others != 0);
   if (lane == 0) found[part * WAVES + wave] = mine;

@@ -157,7 +157,8 @@ __global__ __launch_bounds__(WAVES *GROUPS *kWave, 2) void attention_kernel(Atte
     // that repeat or overlap stand behind the last key too, where others are zeros.)
     auto round_of = [&](LdsChunks k, LdsChunks v, int n) __attribute__((always_inline)) {
       if ((p.causal || p.v.token < dim) && seen.tile_all - n * GROUPS * BN < GROUPS * BN &&
-          clean<T, L::SIZE, WAVES, GROUPS>(v, found, wave, part, lane))
+          clean<T, L::SIZE, WAVES, GROUPS>(v, (n * GROUPS + part) * BN < keys.count, found, wave,
+                                           part, lane))
         loose = loose < 0 ? n : loose;
       work(k, v, n);
     };

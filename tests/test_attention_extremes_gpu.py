@@ -120,3 +120,46 @@ def test_attention_of_repeated_values_that_are_not_finite(lengths, heads, causal
     want, wlse = fw.attention_packed(q, k, over.contiguous(), off, causal=causal)
     assert torch.equal(lse, wlse) and torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
     assert not out.isnan().any() and out.isinf().any()
+
+
+def _after_junk(value, kind, call, times):
+    """`call` after one that leaves `value` all over LDS: its results and its times in us."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    junk = torch.full((4000, 32, 64), value, dtype=_dt(kind), device="cuda")
+    off = torch.tensor([0, 4000], dtype=torch.int32, device="cuda")
+    out, us = [], []
+    for _ in range(times):
+        fw.attention_packed(junk, junk, junk, off, causal=False)
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        out.append(call())
+        end.record()
+        end.synchronize()
+        us.append(begin.elapsed_time(end) * 1e3)
+    return out, us
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[330, 40, 64, 1], [129, 300, 65, 160], [148] * 4])
+def test_attention_of_sequences_that_leave_a_group_without_a_tile(lengths, kind):
+    """Of two groups of waves one finds no keys in some rounds; what its part of LDS
+    holds then, here the NaN of another call, is nobody's."""
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, v, _ = _packed_inputs(lengths, None, 2, 2, 64, kind)
+    want = _attention_want(q, k, v, off, None, True, 0.125, kind)
+    args = [t.cuda() for t in (q, k, v, off)]
+    for out, lse in _after_junk(math.nan, kind, lambda: fw.attention_packed(*args), 3)[0]:
+        _assert_within(_np64(out), want[0], want[1], "out")
+        _assert_within(_np64(lse), want[2], want[3], "lse")
+
+
+def test_attention_takes_no_longer_for_what_others_left_in_lds():
+    """(Taken for values that are not finite, it made a call of 10 us one of 62.)"""
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, v, _ = _packed_inputs([148] * 4, None, 8, 8, 64, "bf16")
+    args = [t.cuda() for t in (q, k, v, off)]
+    times = [np.median(_after_junk(value, "bf16", lambda: fw.attention_packed(*args), 20)[1])
+             for value in (1.0, math.nan)]
+    assert times[1] < 3 * times[0], times

@@ -245,8 +245,10 @@ def attention_packed(q, k, v, offsets, kv_offsets=None, causal=True, scale=None,
     out, ot, oh = _rows_out(torch, out, "out", (n, heads, dim), q, stream, dtype, dev)
     if lse is None:
         lse = _new(torch, (n, heads), q, stream, torch.float32)
-    elif lse.shape != (n, heads):
-        raise ValueError("lse must be (tokens, heads)")
+    else:
+        _on(torch, lse, "lse", dev)
+        if lse.shape != (n, heads):
+            raise ValueError("lse must be (tokens, heads)")
     status = lib.attention_packed(*sizes, *rows, off, koff, 1 if causal else 0, scale, fill,
                                   out.data_ptr(), ot, oh,
                                   _vector(torch, lse, "lse", n * heads, dev),

@@ -163,3 +163,16 @@ def test_attention_takes_no_longer_for_what_others_left_in_lds():
     times = [np.median(_after_junk(value, "bf16", lambda: fw.attention_packed(*args), 20)[1])
              for value in (1.0, math.nan)]
     assert times[1] < 3 * times[0], times
+
+
+def test_attention_refuses_logarithms_that_are_no_tensor():
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, v, _ = (None if t is None else t.cuda()
+                          for t in _packed_inputs([20], None, 2, 2, 64, "f32"))
+    for lse in ([0.0] * 20, np.zeros((20, 2), np.float32)):
+        with pytest.raises(TypeError, match="lse"):
+            fw.attention_packed(q, k, v, off, lse=lse)
+    with pytest.raises(ValueError, match="lse"):
+        fw.attention_packed(q, k, v, off, lse=torch.zeros(20, 2))

@@ -176,3 +176,44 @@ def test_attention_refuses_logarithms_that_are_no_tensor():
             fw.attention_packed(q, k, v, off, lse=lse)
     with pytest.raises(ValueError, match="lse"):
         fw.attention_packed(q, k, v, off, lse=torch.zeros(20, 2))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths,heads", [([1] * 40 + [900] + [2] * 30, 8), ([1] * 9 + [900], 8),
+                                           ([0] * 200 + [700, 0, 3], 2), ([3000] + [10] * 99, 1)])
+def test_attention_of_one_long_sequence_among_short_ones(lengths, heads, kind):
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, v, grad = _packed_inputs(lengths, None, heads, max(1, heads // 4), 64, kind)
+    out, lse = fw.attention_packed(q.cuda(), k.cuda(), v.cuda(), off.cuda())
+    want = _attention_want(q, k, v, off, None, True, 0.125, kind)
+    _assert_within(_np64(out), want[0], want[1], "out")
+    _assert_within(_np64(lse), want[2], want[3], "lse")
+    got = fw.attention_packed_grad(grad.cuda(), q.cuda(), k.cuda(), v.cuda(), out, lse, off.cuda())
+    want, tol = _gradient_want(grad, q, k, v, out, lse, off, None, True, 0.125, kind)
+    for a, w, t, what in zip(got, want, tol, "qkv"):
+        _assert_within(_np64(a), w, t, what)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[20, 7], [100, 90], [301]])
+def test_attention_without_its_logarithms(lengths, kind):
+    """lse may be NULL for the C entry point, fill asking for it or not."""
+    import torch
+
+    import dlrm_embedding_bag_amd as fw
+    off, _, q, k, v, _ = (None if t is None else t.cuda()
+                          for t in _packed_inputs(lengths, None, 2, 2, 64, kind))
+    n = len(q)
+    off = torch.cat((off, off[-1:] + 0))[1:].contiguous()     # rows before the first sequence
+    want, _ = fw.attention_packed(q, k, v, off)
+    for fill in (0, 1, 2, 3):
+        out = torch.full_like(q, 7.0)
+        row = (128, 64)
+        status = fw.load().attention_packed(
+            n, n, len(off) - 1, 2, 2, 64, 0 if kind == "f32" else 1, q.data_ptr(), *row,
+            k.data_ptr(), *row, v.data_ptr(), *row, off.data_ptr(), None, 1, 0.125, fill,
+            out.data_ptr(), *row, None, torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        first = int(off[0])
+        assert torch.equal(out[first:], want[first:])
+        assert (out[:first] == (0.0 if fill & 1 else 7.0)).all()

@@ -5,9 +5,11 @@
 //
 // Bounded by the cache's bytes: every code is read once, for all heads that share
 // its key head (16 of them at a time are the columns of 16 x 16 products; fewer
-// leave columns idle, which costs matrix time that there is plenty of).  A wave
-// walks 64 keys a step.  Codes become bfloat16 (float32 for float32 queries) by
-// the conversion instructions, which take the group's scale along and are exact.
+// leave columns idle, which costs matrix time that there is plenty of for bfloat16
+// queries, but not for float32 ones).  A wave walks 64 keys a step.  Codes become
+// bfloat16 (float32 for float32 queries) by the conversion instructions, which take
+// the group's scale along and are exact; the weights are rounded to bfloat16 for
+// bfloat16 queries.
 //
 // No value passes between lanes: in s^T = k q^T a lane holds a key's share of its
 // dim, D/4 neighbouring elements (one load), the same ones of its head's query;
@@ -18,9 +20,9 @@
 //
 // Long sequences are split over workgroups, each sequence into equal shares of
 // its own length; the shares' maxima, sums and outputs meet in a second kernel.
-// (64 sequences of up to 8000 keys, 8 key heads of 128 in 8 bits: 118 us, 5.1 TB/s;
-// one of 131001 in 4 bits 33 us, 4.3 TB/s, both after their shares' meeting 5 and 2
-// us later.)
+// (64 sequences of up to 8000 keys, 8 key heads of 128 in 8 bits, 32 bfloat16 heads: 120
+// us, 5.0 TB/s; one of 131001 in 4 bits 31 us, 4.6 TB/s; their shares' meeting 5 us more
+// each.  For float32 heads the two take 237 and 92 us for 127 and 36 in all.)
 #include <math.h>
 
 #include "attention_common.hpp"
@@ -386,8 +388,9 @@ int head_tiles_of(int group) { return (group + kHeads - 1) / kHeads; }
 
 // Shares of a sequence: two workgroups a CU (one sequence of 131001 keys, 8 key heads
 // of 128 in 4 bits: 64 shares 35 us, 32 43, 128 42), or where sequences are many,
-// four shares each, since the long ones among them would end last; none with less
-// than a step for each of its waves.
+// four shares each, since the long ones among them would end last; no more than its
+// row of the table has steps for.  A sequence shorter than that row leaves shares
+// empty (64 of 50 keys take 26 us under rows of 1024 keys as of 131072).
 int splits_of(int64_t batch, int heads, int kv_heads, int64_t max_pages, int page) {
   const int64_t groups = batch * kv_heads * head_tiles_of(heads / kv_heads);
   const int64_t most = (max_pages * page + kWaves * kStep - 1) / (kWaves * kStep);

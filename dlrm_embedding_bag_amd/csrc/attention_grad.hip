@@ -12,8 +12,10 @@
 // side by side for the second, whose workgroups own keys and walk rows and heads.
 // The scores are made twice for that: seven products of scores' size instead of
 // five.  (Three sequences of up to 5000 rows, 32 heads of 128 in bfloat16: 570 us and
-// 900, 680 TFLOP/s of the five products, 950 of the seven.)  Both keep scores transposed or not so that p and ds, made in registers,
-// are operands of the next product where they stand, as in the forward pass.
+// 900 to 930, 680 TFLOP/s of the five products, 950 of the seven.)  Both keep scores
+// transposed or not so that p and ds, made in registers, are operands of the next product
+// where they stand, as in the forward pass; for bfloat16 rows both are rounded to bfloat16
+// for it, which the matrix cores take at many times the rate of float32.
 #include <math.h>
 
 #include "attention_common.hpp"

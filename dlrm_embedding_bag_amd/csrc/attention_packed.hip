@@ -10,11 +10,16 @@
 // the operand of out^T += v^T p^T without leaving the registers; keys and values
 // pass through LDS, the next tile on its way while one is worked on.
 //
-// In bfloat16 of 128 elements a tile's products, its exponentials and its reads of LDS
-// take about as long as each other, so two waves a SIMD cover each other.  (Four
-// prompts of up to 6500 rows, 32 heads: 800 us, 1000 TFLOP/s; a single wave a SIMD with
-// 64 rows, which halves the reads, 1207.  In float32 four of up to 3000 rows 117 TFLOP/s of
-// the 154 that the matrix cores give a library's product.)
+// For bfloat16 rows the weights are rounded to bfloat16, which a library's product takes
+// at nine times the rate of float32 (1400 for 154 TFLOP/s); their sum l takes them whole.
+// (Against 64 bits the prompts' outputs are off by 0.0021 of their size, by 0.0016 where
+// nothing but they themselves is rounded.)
+//
+// In bfloat16 of 128 elements the matrix cores are busy 48% of the time; between a wave's
+// products stand its exponentials and its reads of LDS, and two waves a SIMD cover each
+// other.  (Four prompts of up to 6500 rows, 32 heads: 800 to 850 us by card and run, 1000
+// to 940 TFLOP/s; a single wave a SIMD with 64 rows, which halves the reads, 1207.  In
+// float32 four of 1500 to 3000 rows 118 TFLOP/s.)
 #include <math.h>
 
 #include "attention_forward.hpp"
@@ -247,6 +252,9 @@ hipError_t by_size(const AttentionParams &p, hipStream_t stream) {
 
 }  // namespace
 
+// Kernels go by the means of a call's sequences, since offsets are not read on the host:
+// a long sequence among many short ones is walked by their kernel (32 heads of 128 in
+// bfloat16: one of 2000 rows 53 us, beside 64 of one row 189; one of 4000 150 and 193).
 hipError_t launch_attention(const AttentionParams &p, int dtype, hipStream_t stream) {
   // tiles of 16 rows for sequences of few (8 heads, the mean of their rows: in float32
   // of 64 elements 10 42 us for 83, 40 26 for 35; in bfloat16 of 128 10 54 for 80, 40 23

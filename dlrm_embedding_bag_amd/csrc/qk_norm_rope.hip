@@ -14,7 +14,7 @@
 // thread, and leave them in LDS, where all heads of a token find them.  Then
 // every group of lanes takes a row, each lane both members of its pairs, so a
 // row never leaves its lanes' registers.  (16384 tokens of 40 heads of 128 in
-// bfloat16: 68 us, 4.9 TB/s; the gradient of 8191 of 20 of 96 in float32 49 us.)
+// bfloat16: 69 us, 4.8 TB/s; the gradient of 8191 of 20 of 96 in float32 51 us.)
 #include <math.h>
 
 #include "kernels.hpp"
@@ -338,7 +338,8 @@ bool many(int64_t tokens) { return tokens >= 1024; }
 // Four tokens or more, where few and short rows would leave lanes without one (28785
 // tokens of 4 + 2 heads of 8 in bfloat16: 12 us for 18, gradient 24 for 51; 100000 of
 // 1 + 1 of 64 34 for 105 and 63 for 182): as many as LDS holds the turns of, and
-// workgroups are left for all CUs.
+// workgroups are left for all CUs.  (The last of these still use 64 of the 256 threads,
+// 16 tokens of 4 lanes, for q and again for k.)
 int tokens_each(const RopeParams &p, int lanes) {
   if (!many(p.tokens)) return 1;
   const int heads = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;

@@ -690,9 +690,9 @@ DLRM_API int linear_i8_bias_act(int32_t m, int32_t n, int32_t k, const int8_t *a
  *   pair i of v, (a, b)  ->  (a cos(t f) - b sin(t f), a sin(t f) + b cos(t f))
  * with t = positions[token] and f = freqs[i].  Pairs are elements (i, i + pairs),
  * or (2 i, 2 i + 1) if interleaved; elements from 2 * pairs on are not turned.
- * The mean and the angle t f are in float64, so positions may lie far out; the
- * result is rounded once.  An infinity or a NaN in a row leaves NaN in that row
- * only.
+ * The mean, its root and the angle t f are in float64, so positions may lie far
+ * out; what follows is float32 arithmetic, rounded once more where the result is
+ * bfloat16.  An infinity or a NaN in a row leaves NaN in that row only.
  *
  *   tokens     0 <= tokens <= INT32_MAX (0: nothing to do)
  *   heads, kv_heads  >= 0, not both 0 (0: q or k is not used and may be NULL)
@@ -715,8 +715,8 @@ DLRM_API int qk_norm_rope(int64_t tokens, int32_t heads, int32_t kv_heads, int32
 /*
  * qk_norm_rope_grad -- the gradients of qk_norm_rope, from those of its outputs
  * and its inputs:
- *   out_q, out_k                gradients of q and k, rounded once; may be the
- *                               incoming gradients or q and k themselves
+ *   out_q, out_k                gradients of q and k; may be the incoming
+ *                               gradients or q and k themselves
  *   out_q_weight, out_k_weight  (dim,) float32 gradients of the weights, sums
  *                               over all tokens and heads in a fixed order, or
  *                               NULL where they are not wanted
@@ -745,10 +745,12 @@ DLRM_API int qk_norm_rope_grad(
  *   out    = sum_j exp(s[j] - lse) v[j, g]
  * With causal the last query sees all keys, the one before it all but the last,
  * and so on, so that a sequence with more keys than queries continues one.  A
- * row that sees no key (or whose scores are all -inf) has out 0 and lse -inf.
- * What a row does not see does not reach it, not as a NaN either.
- * For bfloat16 inputs exp(s - m) of each row's running maximum m is rounded to
- * bfloat16 before it meets the values; out is rounded once.
+ * row that sees no key (or whose scores are all -inf and its values finite) has
+ * out 0 and lse -inf.  What a row does not see does not reach it, not as a NaN
+ * either.
+ * For bfloat16 inputs the weights are rounded to bfloat16 before they meet the
+ * values, as exp(s - m) of a reference m that follows each row's running maximum
+ * and lies up to 8 log(2) below it; lse takes them whole, out is rounded once.
  *
  *   tokens, kv_tokens  rows of q and out, and of k and v; up to INT32_MAX
  *   batch       sequences, 1 <= batch < INT32_MAX; sequences may be empty
